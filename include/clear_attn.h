@@ -55,7 +55,9 @@ typedef enum {
   CLEAR_ERR_UNSUPPORTED = 2,      /* d not in {64, 128}, or no sm_100 device */
   CLEAR_ERR_WORKSPACE = 3,        /* workspace missing or smaller than the queried size */
   CLEAR_ERR_CUDA = 4,             /* a CUDA runtime/driver call failed (launch, tensor map) */
-  CLEAR_ERR_DEVICE_TIMEOUT = 5    /* a kernel's bounded wait expired (reported by clear_attn_check) */
+  CLEAR_ERR_DEVICE_TIMEOUT = 5,   /* a kernel's bounded wait expired (reported by clear_attn_check) */
+  CLEAR_ERR_DEVICE_INDEX = 6      /* an offset, length or page number in device memory was out of range;
+                                     it was skipped (reported by clear_attn_check) */
 } clear_status_t;
 
 /* Problem description. All fields are plain element counts. */
@@ -363,7 +365,8 @@ CLEAR_API clear_status_t clear_attn_bwd(const clear_attn_params_t* params, const
 
 /* Synchronises `stream`, then reads and clears the device error word of the current device.
  * Returns CLEAR_OK, CLEAR_ERR_DEVICE_TIMEOUT (a kernel gave up a bounded wait; its outputs are
- * invalid) or CLEAR_ERR_CUDA (the stream reported a CUDA error). */
+ * invalid), CLEAR_ERR_DEVICE_INDEX (a token-sequence operator met an index out of range in device
+ * memory) or CLEAR_ERR_CUDA (the stream reported a CUDA error). */
 CLEAR_API clear_status_t clear_attn_check(void* stream);
 
 /* Context of the expired wait behind the last CLEAR_ERR_DEVICE_TIMEOUT that clear_attn_check()
@@ -384,6 +387,117 @@ CLEAR_API void clear_attn_device_diag(int* out8);
  * CLEAR_ERR_CUDA if the launch fails. It shares the device error word with every other call on
  * the device: do not run it concurrently with attention calls whose status you need. */
 CLEAR_API clear_status_t clear_attn_selftest_expiry(int limit_ms, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Token sequences: attention over plain sequences of tokens with causal masks, grouped heads and
+ * a paged key/value cache, for the language models next to such a transformer (text conditioning,
+ * prompt rewriting, captioning). The CLEAR paper has no counterpart.
+ *
+ * A packed batch holds n_seq sequences one after another along the token axis: sequence s has the
+ * tokens [seq_start[s], seq_start[s + 1]). q, o and the like are [q_heads, n_tok, d], k and v
+ * [kv_heads, n_tok, d], as views with any head and token strides; query head h reads key/value head
+ * h / (q_heads / kv_heads). Scores are scaled by 1/sqrt(d). Elements are bf16 or fp16.
+ *
+ * A paged cache keeps keys and values in pages of page_size tokens: token p of sequence s lies in row
+ * p % page_size of page page_table[s][p / page_size]. Table entries behind a sequence's last page
+ * are never read. Pages may be shared by sequences for reading; two new tokens must not share a row.
+ *
+ * seq_start (int32 [n_seq + 1]), seq_len (int32 [n_seq]) and the page table are device memory, read
+ * when the kernels run: a captured graph may be replayed with other contents. The kernels check them. A
+ * sequence whose offsets decrease or leave [0, n_tok], or a page number outside [0, n_pages) or past
+ * max_pages, is skipped (a skipped page reads as zeros) and clear_attn_check() reports
+ * CLEAR_ERR_DEVICE_INDEX. Tokens behind the last sequence are neither read nor written.
+ *
+ * Statuses: CLEAR_ERR_INVALID_ARG for null or misaligned (16 bytes) pointers, sizes out of range
+ * (n_seq in [1, 2^20], n_tok in [1, 2^30]), q_heads not a multiple of kv_heads;
+ * CLEAR_ERR_UNSUPPORTED for d other than 64 and 128, other types, or a stride of an axis with more
+ * than one element that is not a positive multiple of 16 bytes.
+ * --------------------------------------------------------------------------------------------- */
+enum { CLEAR_DTYPE_BF16 = 0, CLEAR_DTYPE_FP16 = 1, CLEAR_DTYPE_E4M3 = 2 };
+enum { CLEAR_PAIR_ADJACENT = 0, CLEAR_PAIR_HALVES = 1 };
+
+typedef struct {
+  int n_seq;               /* sequences */
+  int n_tok;               /* tokens along the packed axis (rows behind the last sequence included) */
+  int q_heads, kv_heads;   /* q_heads a multiple of kv_heads */
+  int d;                   /* head dim: 64 or 128 */
+  int dtype;               /* CLEAR_DTYPE_BF16 or CLEAR_DTYPE_FP16 */
+} clear_seq_params_t;
+
+/* A [heads, tokens, d] view: element (h, t, i) at ptr + h * head_stride + t * token_stride + i
+ * (strides in elements; the stride of an axis of one element is not used). */
+typedef struct {
+  void* ptr;
+  long long head_stride, token_stride;
+} clear_seq_view_t;
+
+typedef struct {
+  void *k_pages, *v_pages;           /* pages of dtype; element (page, row, head, i) at the strides below */
+  const int* page_table;             /* device int32 [n_seq][page_table_stride] */
+  const float *k_scale, *v_scale;    /* E4M3: device fp32 [kv_heads], a code stands for code * scale; else unused */
+  long long k_strides[3], v_strides[3]; /* {page, token, head} in elements; the d elements are contiguous */
+  long long page_table_stride;       /* entries between two sequences' rows, >= max_pages */
+  int n_pages, page_size, max_pages; /* pages in k_pages and v_pages; tokens per page; entries per sequence */
+  int dtype;                         /* the params' dtype, or CLEAR_DTYPE_E4M3 */
+} clear_seq_cache_t;
+
+/* Rotary embedding of the first `rot` elements of each head (a multiple of 16, at most d; 0: none):
+ * pair i of rot/2 turns by position * base^(-2i/rot), base = theta * ntk^(rot/(rot - 2)), theta > 1,
+ * ntk > 0. pairing: CLEAR_PAIR_ADJACENT pairs elements 2i and 2i+1 (as clear_attn_rope does on each
+ * axis), CLEAR_PAIR_HALVES elements i and i + rot/2. */
+typedef struct {
+  float theta, ntk;
+  int rot, pairing;
+} clear_seq_rope_t;
+
+/*
+ * Appends the packed tokens' keys and values to the cache, rotating queries and keys on the way.
+ * seq_len[s] is the sequence's length in the cache AFTER the call: token t of sequence s has
+ * position seq_len[s] - (seq_start[s + 1] - t). A token of negative position (a padded slot, with
+ * seq_len 0) is left out. Angles are taken in double, so far positions are as exact as near ones.
+ *   rope    NULL or rot = 0: nothing is rotated.
+ *   q       may be NULL (with q_out); q_out receives the rotated queries, and may be q itself.
+ *   k, v    new keys and values; rotated keys and values go to the cache (E4M3: rounded to nearest
+ *           from the fp32 rotated value over the scale, saturated at 448).
+ *   k_out   NULL, or receives the rotated keys (packed), and may be k itself.
+ * Only the new tokens' rows of the cache are written. Two tokens that the page table sends to the
+ * same row (a page listed twice where both write) leave that row undefined.
+ */
+CLEAR_API clear_status_t clear_attn_cache_append(const clear_seq_params_t* params, const clear_seq_cache_t* cache,
+                                                 const clear_seq_rope_t* rope, const int* seq_start, const int* seq_len,
+                                                 const clear_seq_view_t* q, const clear_seq_view_t* k,
+                                                 const clear_seq_view_t* v, const clear_seq_view_t* q_out,
+                                                 const clear_seq_view_t* k_out, void* stream);
+
+/* Workspace bytes of clear_attn_decode (they do not depend on the sequences or their lengths). */
+CLEAR_API size_t clear_attn_decode_workspace_size(const clear_seq_params_t* params, clear_status_t* status);
+
+/*
+ * Attention of one token per sequence over its cached keys and values: n_tok = n_seq, token s is
+ * sequence s's query, and it attends to the first seq_len[s] rows of the sequence's pages.
+ *   q, o   [q_heads, n_seq, d]; lse: fp32 [q_heads, n_seq] contiguous, or NULL
+ *   A sequence with seq_len <= 0 gets o = 0 and lse = -inf, and so does a row all of whose scores are -inf.
+ *   workspace: clear_attn_decode_workspace_size bytes, 256-byte aligned; its contents need not be
+ *   set and are undefined on return; calls that overlap on the GPU must not share one.
+ * Two kernels are launched (the second joins the split sequences); results do not depend on
+ * scheduling: the same call gives the same bits. What lies in the pages behind a sequence's end
+ * does not count, NaN included.
+ */
+CLEAR_API clear_status_t clear_attn_decode(const clear_seq_params_t* params, const clear_seq_cache_t* cache,
+                                           const int* seq_len, const clear_seq_view_t* q, const clear_seq_view_t* o,
+                                           float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Causal attention within each sequence of a packed batch: token i attends to the tokens j <= i of its sequence.
+ *   q, o [q_heads, n_tok, d]; k, v [kv_heads, n_tok, d]; lse: fp32 [q_heads, n_tok] contiguous, natural
+ *   log of the softmax denominator of the scaled scores, or NULL.
+ * A sequence's results do not depend on what the others hold. Within one sequence a NaN or infinity in v
+ * reaches the rows from its own block of 128 tokens on (a zero probability times NaN is NaN).
+ */
+CLEAR_API clear_status_t clear_attn_prompt_fwd(const clear_seq_params_t* params, const int* seq_start,
+                                               const clear_seq_view_t* q, const clear_seq_view_t* k,
+                                               const clear_seq_view_t* v, const clear_seq_view_t* o, float* lse,
+                                               void* stream);
 
 /* ---------------------------------------------------------------------------------------------
  * Host-only scheduler queries (no GPU needed). They expose the tile enumeration the kernels use,

@@ -17,12 +17,20 @@ _EXPORTS = {
     "clear_attn_rope", "rope_rotate_workspace_size", "clear_attn_bwd_rope",
 }
 
+# Token-sequence operators: paged cache, decode, causal packed attention.
+_SEQUENCE_EXPORTS = {
+    "clear_attn_cache_append", "clear_attn_decode", "clear_attn_prompt_fwd", "clear_attn_prompt_bwd",
+    "decode_workspace_size", "prompt_bwd_workspace_size",
+}
+
 
 def __getattr__(name):
     if name in _EXPORTS:
         return getattr(importlib.import_module("._binding", __name__), name)
+    if name in _SEQUENCE_EXPORTS:
+        return getattr(importlib.import_module("._sequence", __name__), name)
     raise AttributeError(name)
 
 
 def __dir__():
-    return sorted(_EXPORTS)
+    return sorted(_EXPORTS | _SEQUENCE_EXPORTS)

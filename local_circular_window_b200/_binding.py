@@ -23,7 +23,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 CLEAR_OK = 0
 STATUS_NAMES = {0: "CLEAR_OK", 1: "CLEAR_ERR_INVALID_ARG", 2: "CLEAR_ERR_UNSUPPORTED", 3: "CLEAR_ERR_WORKSPACE",
-                4: "CLEAR_ERR_CUDA", 5: "CLEAR_ERR_DEVICE_TIMEOUT"}
+                4: "CLEAR_ERR_CUDA", 5: "CLEAR_ERR_DEVICE_TIMEOUT", 6: "CLEAR_ERR_DEVICE_INDEX"}
 
 
 class ClearStrides(ctypes.Structure):

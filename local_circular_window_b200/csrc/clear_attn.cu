@@ -785,6 +785,7 @@ const char* clear_status_string(clear_status_t s) {
     case CLEAR_ERR_WORKSPACE: return "CLEAR_ERR_WORKSPACE";
     case CLEAR_ERR_CUDA: return "CLEAR_ERR_CUDA";
     case CLEAR_ERR_DEVICE_TIMEOUT: return "CLEAR_ERR_DEVICE_TIMEOUT";
+    case CLEAR_ERR_DEVICE_INDEX: return "CLEAR_ERR_DEVICE_INDEX";
   }
   return "CLEAR_ERR_UNKNOWN";
 }
@@ -1176,7 +1177,7 @@ clear_status_t clear_attn_check(void* stream) {
       return CLEAR_ERR_CUDA;
     const int zero = 0;
     cudaMemcpyToSymbol(clear::g_clear_device_error, &zero, sizeof(int));
-    return CLEAR_ERR_DEVICE_TIMEOUT;
+    return err == clear::kDevBadIndex ? CLEAR_ERR_DEVICE_INDEX : CLEAR_ERR_DEVICE_TIMEOUT;
   }
   return CLEAR_OK;
 }
@@ -1293,3 +1294,5 @@ clear_status_t clear_sched_pair_counts(const clear_attn_params_t* params, long l
 }
 
 }  // extern "C"
+
+#include "clear_seq_host.cuh"

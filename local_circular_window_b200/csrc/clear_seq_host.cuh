@@ -1,0 +1,271 @@
+// Host side of the token-sequence operators (declared in include/clear_attn.h): argument checks,
+// tensor maps and launches. Included by clear_attn.cu.
+#pragma once
+
+#include "clear_seq_append.cuh"
+#include "clear_seq_decode.cuh"
+#include "clear_seq_prompt.cuh"
+
+namespace {
+
+bool seq_strides_ok(long long s, long long per16, long long n) {
+  // A stride that is used (more than one element along its axis) is a positive multiple of 16 bytes.
+  return n <= 1 || (s > 0 && s % per16 == 0 && s < (1ll << 39));
+}
+
+clear_status_t check_seq_params(const clear_seq_params_t* p) {
+  if (!p) return CLEAR_ERR_INVALID_ARG;
+  if (p->n_seq < 1 || p->n_seq > (1 << 20) || p->n_tok < 1 || p->n_tok > (1 << 30)) return CLEAR_ERR_INVALID_ARG;
+  if (p->q_heads < 1 || p->kv_heads < 1 || p->q_heads > (1 << 14) || p->q_heads % p->kv_heads) return CLEAR_ERR_INVALID_ARG;
+  if (p->dtype != CLEAR_DTYPE_BF16 && p->dtype != CLEAR_DTYPE_FP16) return CLEAR_ERR_UNSUPPORTED;
+  if (p->d != 64 && p->d != 128) return CLEAR_ERR_UNSUPPORTED;
+  return CLEAR_OK;
+}
+
+// A [heads, tokens, d] view: 16-byte aligned, strides of used axes positive multiples of 16 bytes.
+// An unused axis gets a harmless stride.
+clear_status_t check_seq_view(const clear_seq_view_t* v, int heads, int n_tok, int d, SeqView* out) {
+  if (!v || !aligned16(v->ptr)) return CLEAR_ERR_INVALID_ARG;
+  if (!seq_strides_ok(v->head_stride, 8, heads) || !seq_strides_ok(v->token_stride, 8, n_tok)) return CLEAR_ERR_UNSUPPORTED;
+  out->ptr = v->ptr;
+  out->sh = heads > 1 ? v->head_stride : (long long)d;
+  out->st = n_tok > 1 ? v->token_stride : (long long)d;
+  return CLEAR_OK;
+}
+
+clear_status_t check_seq_cache(const clear_seq_params_t* p, const clear_seq_cache_t* c, SeqCache* out) {
+  if (!c) return CLEAR_ERR_INVALID_ARG;
+  if (c->dtype != p->dtype && c->dtype != CLEAR_DTYPE_E4M3) return CLEAR_ERR_UNSUPPORTED;
+  if (c->n_pages < 1 || c->page_size < 1 || c->page_size > (1 << 20) || c->max_pages < 1) return CLEAR_ERR_INVALID_ARG;
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || !c->page_table) return CLEAR_ERR_INVALID_ARG;
+  if (c->page_table_stride < c->max_pages && p->n_seq > 1) return CLEAR_ERR_INVALID_ARG;
+  const bool f8 = c->dtype == CLEAR_DTYPE_E4M3;
+  if (f8 && (!c->k_scale || !c->v_scale)) return CLEAR_ERR_INVALID_ARG;
+  const long long per16 = f8 ? 16 : 8;
+  const int n[3] = {c->n_pages, c->page_size, p->kv_heads};
+  for (int i = 0; i < 3; ++i) {
+    if (!seq_strides_ok(c->k_strides[i], per16, n[i]) || !seq_strides_ok(c->v_strides[i], per16, n[i])) return CLEAR_ERR_UNSUPPORTED;
+    out->ks[i] = n[i] > 1 ? c->k_strides[i] : 0;
+    out->vs[i] = n[i] > 1 ? c->v_strides[i] : 0;
+  }
+  out->k = c->k_pages;
+  out->v = c->v_pages;
+  out->table = c->page_table;
+  out->table_stride = c->page_table_stride;
+  out->max_pages = c->max_pages;
+  out->n_pages = c->n_pages;
+  out->page_size = c->page_size;
+  out->page_div = make_fast_div(c->page_size);
+  out->k_scale = f8 ? c->k_scale : nullptr;
+  out->v_scale = f8 ? c->v_scale : nullptr;
+  return CLEAR_OK;
+}
+
+// ---------------------------------------------------------------------------------------- append
+template <typename E, bool kF8, int D, bool kHalves>
+clear_status_t launch_append(const SeqAppendParams& a, cudaStream_t stream) {
+  // Four tokens a block share the block's set-up; with few tokens one each spreads them over the SMs.
+  if (a.n_tok >= 4096)
+    clear_seq_append_kernel<E, kF8, D, kHalves, 4><<<(a.n_tok + 3) / 4, kAppendThreads, 0, stream>>>(a);
+  else
+    clear_seq_append_kernel<E, kF8, D, kHalves, 1><<<a.n_tok, kAppendThreads, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? CLEAR_OK : CLEAR_ERR_CUDA;
+}
+
+template <typename E, bool kF8>
+clear_status_t launch_append_d(const SeqAppendParams& a, int d, bool halves, cudaStream_t s) {
+  if (d == 64) return halves ? launch_append<E, kF8, 64, true>(a, s) : launch_append<E, kF8, 64, false>(a, s);
+  return halves ? launch_append<E, kF8, 128, true>(a, s) : launch_append<E, kF8, 128, false>(a, s);
+}
+
+// ---------------------------------------------------------------------------------------- decode
+// Blocks of the decode grid: two per SM, as many as are resident at once.
+constexpr int kDecMaxBlocks = 2 * 160;
+
+struct DecodeWorkspace {
+  size_t ml_off, split_off, total;
+};
+DecodeWorkspace decode_workspace_layout(int d) {
+  DecodeWorkspace w;
+  w.ml_off = align256((size_t)2 * kDecMaxBlocks * kDecRows * d * sizeof(float));
+  w.split_off = align256(w.ml_off + (size_t)2 * kDecMaxBlocks * kDecRows * sizeof(float2));
+  w.total = align256(w.split_off + (size_t)kDecMaxBlocks * sizeof(int4));
+  return w;
+}
+
+template <typename E, bool kF8, int D>
+clear_status_t launch_decode(const SeqDecodeParams& p, int num_sms, cudaStream_t stream) {
+  using L = DecLayout<kF8, D>;
+  if (cudaFuncSetAttribute(clear_seq_decode_kernel<E, kF8, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem) != cudaSuccess)
+    return CLEAR_ERR_CUDA;
+  const int blocks = 2 * num_sms < kDecMaxBlocks ? 2 * num_sms : kDecMaxBlocks;
+  clear_seq_decode_kernel<E, kF8, D><<<blocks, kDecThreads, L::kSmem, stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return CLEAR_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks, p.group < kDecRows ? p.group : kDecRows);
+  cfg.blockDim = dim3(D);
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, clear_seq_decode_join_kernel<E, D>, p) != cudaSuccess) {
+    cudaGetLastError();
+    return CLEAR_ERR_CUDA;
+  }
+  return CLEAR_OK;
+}
+
+// ---------------------------------------------------------------------------------------- prompt
+// (d, tokens, heads) view with box 64 x 128 x 1, 128-byte swizzle.
+bool make_seq_map(CUtensorMap* m, const SeqView& v, int heads, int n_tok, int d, int dtype, int rows = 128) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)n_tok, (cuuint64_t)heads};
+  cuuint64_t strides[2] = {(cuuint64_t)v.st * 2, (cuuint64_t)v.sh * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, dtype == CLEAR_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, v.ptr, dims,
+             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Blocks for items of `rows` query rows: one per SM, fewer when the batch cannot have so many items.
+unsigned prompt_blocks(const clear_seq_params_t* p, int rows, int heads, int num_sms) {
+  const long long most = ((long long)p->n_tok / rows + p->n_seq) * heads;
+  return (unsigned)(most < num_sms ? most : num_sms);
+}
+
+template <typename E, int D>
+clear_status_t launch_prompt_fwd(const clear_seq_params_t* sp, const SeqView& q, const SeqView& k, const SeqView& v,
+                                 const SeqPromptParams& p, int num_sms, cudaStream_t stream) {
+  using L = PromptLayout<D>;
+  CUtensorMap mq, mk, mv;
+  if (!make_seq_map(&mq, q, sp->q_heads, sp->n_tok, D, sp->dtype) || !make_seq_map(&mk, k, sp->kv_heads, sp->n_tok, D, sp->dtype) ||
+      !make_seq_map(&mv, v, sp->kv_heads, sp->n_tok, D, sp->dtype))
+    return CLEAR_ERR_CUDA;
+  if (cudaFuncSetAttribute(clear_seq_prompt_fwd_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
+    return CLEAR_ERR_CUDA;
+  clear_seq_prompt_fwd_kernel<E, D><<<prompt_blocks(sp, 256, sp->q_heads, num_sms), kPrThreads, L::kAlloc, stream>>>(mq, mk, mv, p);
+  return cudaGetLastError() == cudaSuccess ? CLEAR_OK : CLEAR_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+clear_status_t clear_attn_cache_append(const clear_seq_params_t* params, const clear_seq_cache_t* cache,
+                                       const clear_seq_rope_t* rope, const int* seq_start, const int* seq_len,
+                                       const clear_seq_view_t* q, const clear_seq_view_t* k, const clear_seq_view_t* v,
+                                       const clear_seq_view_t* q_out, const clear_seq_view_t* k_out, void* stream) {
+  clear_status_t st = check_seq_params(params);
+  if (st != CLEAR_OK) return st;
+  SeqAppendParams a{};
+  if ((st = check_seq_cache(params, cache, &a.c)) != CLEAR_OK) return st;
+  if (!seq_start || !seq_len || !k || !v || !q != !q_out) return CLEAR_ERR_INVALID_ARG;
+  if ((st = check_seq_view(k, params->kv_heads, params->n_tok, params->d, &a.k)) != CLEAR_OK) return st;
+  if ((st = check_seq_view(v, params->kv_heads, params->n_tok, params->d, &a.v)) != CLEAR_OK) return st;
+  if (q && ((st = check_seq_view(q, params->q_heads, params->n_tok, params->d, &a.q)) != CLEAR_OK ||
+            (st = check_seq_view(q_out, params->q_heads, params->n_tok, params->d, &a.q_out)) != CLEAR_OK))
+    return st;
+  if (k_out && (st = check_seq_view(k_out, params->kv_heads, params->n_tok, params->d, &a.k_out)) != CLEAR_OK) return st;
+  bool halves = false;
+  if (rope && rope->rot != 0) {
+    if (!(rope->theta > 1.f) || !(rope->ntk > 0.f) || !std::isfinite(rope->theta) || !std::isfinite(rope->ntk)) return CLEAR_ERR_INVALID_ARG;
+    if (rope->pairing != CLEAR_PAIR_ADJACENT && rope->pairing != CLEAR_PAIR_HALVES) return CLEAR_ERR_INVALID_ARG;
+    if (rope->rot < 0 || rope->rot > params->d) return CLEAR_ERR_INVALID_ARG;
+    if (rope->rot % 16) return CLEAR_ERR_UNSUPPORTED;
+    a.rot = rope->rot;
+    halves = rope->pairing == CLEAR_PAIR_HALVES;
+    const double base = (double)rope->theta * std::pow((double)rope->ntk, (double)a.rot / (a.rot - 2));
+    for (int i = 0; i < a.rot / 2; ++i)
+      a.turns[i] = std::pow(base, -2.0 * i / a.rot) / 6.283185307179586476925286766559;
+  }
+  int num_sms = 0;
+  if ((st = check_device(&num_sms)) != CLEAR_OK) return st;
+  a.seq_start = seq_start;
+  a.seq_len = seq_len;
+  a.n_seq = params->n_seq;
+  a.n_tok = params->n_tok;
+  a.q_heads = q ? params->q_heads : 0;
+  a.kv_heads = params->kv_heads;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool f8 = cache->dtype == CLEAR_DTYPE_E4M3;
+  if (params->dtype == CLEAR_DTYPE_BF16)
+    return f8 ? launch_append_d<Bf16, true>(a, params->d, halves, s) : launch_append_d<Bf16, false>(a, params->d, halves, s);
+  return f8 ? launch_append_d<Fp16, true>(a, params->d, halves, s) : launch_append_d<Fp16, false>(a, params->d, halves, s);
+}
+
+size_t clear_attn_decode_workspace_size(const clear_seq_params_t* params, clear_status_t* status) {
+  const clear_status_t st = check_seq_params(params);
+  if (status) *status = st;
+  return st == CLEAR_OK ? decode_workspace_layout(params->d).total : 0;
+}
+
+clear_status_t clear_attn_decode(const clear_seq_params_t* params, const clear_seq_cache_t* cache, const int* seq_len,
+                                 const clear_seq_view_t* q, const clear_seq_view_t* o, float* lse, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  clear_status_t st = check_seq_params(params);
+  if (st != CLEAR_OK) return st;
+  if (params->n_tok != params->n_seq || !seq_len) return CLEAR_ERR_INVALID_ARG;
+  SeqDecodeParams p{};
+  if ((st = check_seq_cache(params, cache, &p.c)) != CLEAR_OK) return st;
+  if ((st = check_seq_view(q, params->q_heads, params->n_tok, params->d, &p.q)) != CLEAR_OK) return st;
+  if ((st = check_seq_view(o, params->q_heads, params->n_tok, params->d, &p.o)) != CLEAR_OK) return st;
+  const DecodeWorkspace wl = decode_workspace_layout(params->d);
+  if (!workspace || workspace_bytes < wl.total || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return CLEAR_ERR_WORKSPACE;
+  int num_sms = 0;
+  if ((st = check_device(&num_sms)) != CLEAR_OK) return st;
+  p.lse = lse;
+  p.seq_len = seq_len;
+  p.n_seq = params->n_seq;
+  p.q_heads = params->q_heads;
+  p.kv_heads = params->kv_heads;
+  p.group = params->q_heads / params->kv_heads;
+  p.m_tiles = (p.group + kDecRows - 1) / kDecRows;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)params->d));
+  char* ws = static_cast<char*>(workspace);
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + wl.ml_off);
+  p.split = reinterpret_cast<int4*>(ws + wl.split_off);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool f8 = cache->dtype == CLEAR_DTYPE_E4M3, bf = params->dtype == CLEAR_DTYPE_BF16;
+  if (params->d == 64) {
+    if (bf) return f8 ? launch_decode<Bf16, true, 64>(p, num_sms, s) : launch_decode<Bf16, false, 64>(p, num_sms, s);
+    return f8 ? launch_decode<Fp16, true, 64>(p, num_sms, s) : launch_decode<Fp16, false, 64>(p, num_sms, s);
+  }
+  if (bf) return f8 ? launch_decode<Bf16, true, 128>(p, num_sms, s) : launch_decode<Bf16, false, 128>(p, num_sms, s);
+  return f8 ? launch_decode<Fp16, true, 128>(p, num_sms, s) : launch_decode<Fp16, false, 128>(p, num_sms, s);
+}
+
+clear_status_t clear_attn_prompt_fwd(const clear_seq_params_t* params, const int* seq_start, const clear_seq_view_t* q,
+                                     const clear_seq_view_t* k, const clear_seq_view_t* v, const clear_seq_view_t* o,
+                                     float* lse, void* stream) {
+  clear_status_t st = check_seq_params(params);
+  if (st != CLEAR_OK) return st;
+  SeqView vq, vk, vv;
+  SeqPromptParams p{};
+  if (!seq_start) return CLEAR_ERR_INVALID_ARG;
+  if ((st = check_seq_view(q, params->q_heads, params->n_tok, params->d, &vq)) != CLEAR_OK) return st;
+  if ((st = check_seq_view(k, params->kv_heads, params->n_tok, params->d, &vk)) != CLEAR_OK) return st;
+  if ((st = check_seq_view(v, params->kv_heads, params->n_tok, params->d, &vv)) != CLEAR_OK) return st;
+  if ((st = check_seq_view(o, params->q_heads, params->n_tok, params->d, &p.o)) != CLEAR_OK) return st;
+  int num_sms = 0;
+  if ((st = check_device(&num_sms)) != CLEAR_OK) return st;
+  p.lse = lse;
+  p.seq_start = seq_start;
+  p.n_seq = params->n_seq;
+  p.n_tok = params->n_tok;
+  p.q_heads = params->q_heads;
+  p.group = params->q_heads / params->kv_heads;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)params->d));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (params->dtype == CLEAR_DTYPE_BF16)
+    return params->d == 64 ? launch_prompt_fwd<Bf16, 64>(params, vq, vk, vv, p, num_sms, s)
+                           : launch_prompt_fwd<Bf16, 128>(params, vq, vk, vv, p, num_sms, s);
+  return params->d == 64 ? launch_prompt_fwd<Fp16, 64>(params, vq, vk, vv, p, num_sms, s)
+                         : launch_prompt_fwd<Fp16, 128>(params, vq, vk, vv, p, num_sms, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,509 @@
+// Causal attention over packed prompts with grouped heads: the forward pass.
+//
+// Row i of a sequence keeps the keys j <= i of its own sequence:
+//   S = Q K^T / sqrt(d), P = e^(S - m), O = P V / sum P, lse = m + log sum P.
+//
+// Bound by the tensor cores and, next to them, by the exponentials: a 128 x 128 tile of S costs
+// 2 * 128 * 128 * d multiply-adds (512 cycles at d = 128) and 16384 exponentials (1024 cycles of the
+// special-function unit), so both are kept busy at once by two query tiles per block.
+//
+// One block per SM walks a list of items, an item being 256 query rows (tiles A and B of 128) of one
+// head of one sequence; each key/value tile of 128 is loaded once for both.
+//   warps 0-3 / 4-7  softmax and epilogue of tile A / B; a thread owns one row (= one TMEM lane)
+//   warp 8           TMA: Q tiles, then K and V tiles through one ring (K0 K1 V0 K2 V1 ...)
+//   warp 9           issues the products: S = Q K^T into TMEM, then O += P V with P from TMEM
+//   warp 10          finds the block's items, ahead of the others, through a small ring
+// TMEM: S of A and B at columns 0 and 128 (P overwrites S, 16-bit, two values a column), O at 256 and 256 + d.
+// While one tile's softmax runs, the other tile's products do: the issuer alternates A, B.
+//
+// Items are ordered by their number of key tiles, the longest first, over all sequences, and dealt to
+// the blocks back and forth, so that every block gets about the same work. Heads of one group follow
+// one another: they read the same keys and values, from L2.
+//
+// The running maximum is followed lazily: O and the sum are rescaled only when a row's maximum has
+// grown by more than 2^8, which changes nothing but rounding. P is rounded to the element type for
+// the second product (half a step of each probability, of random sign); sums are of the unrounded values.
+//
+// Value rows behind the sequence's end belong to the next sequence or to nothing. Their
+// probabilities are zero, but 0 * NaN is not: the issuer clears those rows in shared memory before
+// the tile that holds them is used.
+#pragma once
+#include <type_traits>
+
+#include "clear_common.cuh"
+#include "clear_seq_common.cuh"
+
+namespace clear {
+
+constexpr int kPrThreads = 384;
+constexpr uint32_t kPrRegsLow = 88, kPrRegsHigh = 208;
+static_assert(2 * 128 * kPrRegsHigh + 128 * kPrRegsLow <= 384 * 168, "register split exceeds the launch allocation");
+constexpr int kPrItems = 4;  // item ring
+constexpr float kPrRescale = 8.0f;
+
+struct SeqPromptParams {
+  SeqView o;
+  float* lse;            // [q_heads, n_tok]
+  const int* seq_start;  // [n_seq + 1]
+  int n_seq, n_tok, q_heads, group;
+  float scale_log2;      // log2(e) / sqrt(d)
+};
+
+// A sequence's tokens [first, first + len), cut to the packed tensors; a decreasing or outlying
+// offset leaves it empty.
+__device__ __forceinline__ void seq_range(const int* __restrict__ seq_start, int n_tok, int s, int* first, int* len) {
+  const int a = __ldg(seq_start + s), b = __ldg(seq_start + s + 1);
+  const bool ok = a >= 0 && b >= a && b <= n_tok;
+  *first = ok ? a : 0;
+  *len = ok ? b - a : 0;
+}
+
+// The list of items over all sequences, held by one warp (every lane calls every function). Tile y
+// of the list, in descending order of its level (index among its sequence's tiles).
+struct TileList {
+  const int* seq_start;
+  int n_seq, n_tok, rows;  // rows: query rows of a tile
+  int level;               // the level of the last tile asked for
+  long long above;         // tiles of higher levels
+  __device__ __forceinline__ int tiles_of(int s) const {
+    int a, n;
+    seq_range(seq_start, n_tok, s, &a, &n);
+    return (n + rows - 1) / rows;
+  }
+  // Number of sequences with a tile of this level.
+  __device__ __forceinline__ int at_level(int lv) const {
+    int c = 0;
+    for (int s = threadIdx.x & 31; s < n_seq; s += 32) c += tiles_of(s) > lv;
+    return __reduce_add_sync(0xffffffffu, c);
+  }
+  // Sets up the list; returns its number of tiles.
+  __device__ __forceinline__ long long init(const int* ss, int ns, int nt, int r) {
+    seq_start = ss; n_seq = ns; n_tok = nt; rows = r;
+    long long sum = 0;
+    int top = 0;
+    for (int s = threadIdx.x & 31; s < n_seq; s += 32) {
+      const int n = tiles_of(s);
+      sum += n;
+      top = n > top ? n : top;
+    }
+    #pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    level = __reduce_max_sync(0xffffffffu, top) - 1;
+    above = 0;
+    return sum;
+  }
+  // Tile y (not before the last one asked for): its sequence and level.
+  __device__ __forceinline__ int find(long long y, int* lv) {
+    int n = at_level(level);
+    while (y >= above + n && level > 0) {
+      above += n;
+      --level;
+      n = at_level(level);
+    }
+    *lv = level;
+    int rank = (int)(y - above);  // the rank-th sequence with a tile of this level
+    for (int s0 = 0; s0 < n_seq; s0 += 32) {
+      const int s = s0 + (threadIdx.x & 31);
+      unsigned has = __ballot_sync(0xffffffffu, s < n_seq && tiles_of(s) > level);
+      const int c = __popc(has);
+      if (rank < c) {
+        while (rank-- > 0) has &= has - 1;
+        return s0 + __ffs(has) - 1;
+      }
+      rank -= c;
+    }
+    return 0;
+  }
+};
+
+// Item number of round r for a block: rounds run back and forth over the blocks.
+__device__ __forceinline__ long long deal(int r, int block, int blocks) {
+  return (long long)r * blocks + ((r & 1) ? blocks - 1 - block : block);
+}
+
+template <int D>
+struct PromptLayout {
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kBlock = 128 * 128;               // 128 rows x 64 elements, 128-byte swizzle
+  static constexpr int kStages = D == 128 ? 5 : 8;       // ring of K and V tiles
+  static constexpr int kQ = 0;
+  static constexpr int kRing = kQ + 2 * kTileBytes;
+  static constexpr int kBars = kRing + kStages * kTileBytes;
+  static constexpr int bQFull = 0, bQEmpty = 1;
+  static constexpr int bFull = 2, bEmpty = bFull + kStages;
+  static constexpr int bS = bEmpty + kStages;            // + tile: S written
+  static constexpr int bP = bS + 2;                      // + tile: P written (and O rescaled)
+  static constexpr int bO = bP + 2;                      // + tile: the item's last P V done
+  static constexpr int bItemFull = bO + 2, bItemEmpty = bItemFull + kPrItems;
+  static constexpr int bDrain = bItemEmpty + kPrItems;
+  static constexpr int kNumBars = bDrain + 1;
+  static constexpr int kItems = (kBars + kNumBars * 8 + 15) & ~15;  // int4[kPrItems]
+  static constexpr int kMisc = kItems + kPrItems * 16;
+  static constexpr int kAlloc = kMisc + 16 + 1024;
+  static_assert(kAlloc <= 232448, "shared memory");
+};
+
+template <typename E>
+__host__ __device__ constexpr uint32_t idesc_seq(int M, int N, int a_mn, int b_mn) {
+  return std::is_same<E, Bf16>::value ? idesc_bf16_f32(M, N, a_mn, b_mn)
+                                      : (idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10)));  // fp16: format 0
+}
+
+// One 128-row tile of d columns: tokens from tok of head h.
+template <int D>
+__device__ __forceinline__ void load_seq_tile(uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int tok, int h) {
+  #pragma unroll
+  for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * kHalfBytes, m, bar, c * 64, tok, h);
+}
+
+// Rows [from, 128) of a 128-row tile in shared memory become zero (whole warp).
+template <int D>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int from) {
+  for (int i = threadIdx.x & 31; i < (128 - from) * (D / 8); i += 32) {
+    const int r = from + i / (D / 8), c = i % (D / 8);
+    *reinterpret_cast<uint4*>(tile + (c >> 3) * kHalfBytes + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// mbar_wait for a whole warp: every lane returns the same, so that a warp leaves its loop together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int err_code, int site,
+                                          int c0 = 0, int c1 = 0) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err_code, site, c0, c1));
+}
+
+// After an expired wait: waits, again with a limit, for a copy or product still in flight, whatever
+// the abort flag says, so that nothing writes shared or tensor memory after the block has left.
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_test(bar, parity) && globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(100);
+}
+
+// An item as the ring carries it: {first token of tile A, query rows left from there, tile A's number, head}.
+template <typename E, int D>
+__global__ void __launch_bounds__(kPrThreads, 1)
+clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ SeqPromptParams p) {
+  using L = PromptLayout<D>;
+  using T = typename E::type;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  int4* items = reinterpret_cast<int4*>(smem + L::kItems);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars[L::bQFull], 1);
+    mbar_init(&bars[L::bQEmpty], 1);
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&bars[L::bFull + s], 1);
+      mbar_init(&bars[L::bEmpty + s], 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&bars[L::bS + h], 1);
+      mbar_init(&bars[L::bP + h], 128);
+      mbar_init(&bars[L::bO + h], 1);
+    }
+    for (int i = 0; i < kPrItems; ++i) {
+      mbar_init(&bars[L::bItemFull + i], 1);
+      mbar_init(&bars[L::bItemEmpty + i], 10);  // the loader, the issuer, eight softmax warps
+    }
+    mbar_init(&bars[L::bDrain], 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // The next item; false at the end of the list (or on an expired wait). Whole warp.
+  uint32_t n_item = 0;
+  const auto next_item = [&](int4* it, int site) -> bool {
+    const uint32_t s = n_item % kPrItems;
+    if (!warp_wait(&bars[L::bItemFull + s], (n_item / kPrItems) & 1, abort_flag, kDevTimeoutOther, site, (int)n_item)) return false;
+    *it = items[s];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[L::bItemEmpty + s]);
+    ++n_item;
+    return it->y > 0;
+  };
+
+  if (warp == 8) {
+    // ------------------------------------------------------------------ loader
+    regs_dec<kPrRegsLow>();
+    int4 it;
+    uint32_t n = 0, slot = 0, q_loads = 0;
+    bool ok = true;
+    while (ok && next_item(&it, 40)) {
+      if (lane == 0) {
+        const int hk = it.w / p.group;
+        const bool two = it.y > 128;
+        const int tiles = it.z + (two ? 2 : 1);  // key tiles of the item
+        const int seq0 = it.x - it.z * 128;      // the sequence's first token
+        ok = mbar_wait(&bars[L::bQEmpty], (n & 1) ^ 1, abort_flag, kDevTimeoutTmaEmpty, 1, (int)n);
+        if (ok) {
+          mbar_arrive_expect_tx(&bars[L::bQFull], (two ? 2 : 1) * L::kTileBytes);
+          load_seq_tile<D>(smem + L::kQ, &tm_q, &bars[L::bQFull], it.x, it.w);
+          if (two) load_seq_tile<D>(smem + L::kQ + L::kTileBytes, &tm_q, &bars[L::bQFull], it.x + 128, it.w);
+          ++q_loads;
+        }
+        const auto load = [&](const CUtensorMap* m, int tok) {
+          const uint32_t s = slot % L::kStages;
+          ok = ok && mbar_wait(&bars[L::bEmpty + s], ((slot / L::kStages) & 1) ^ 1, abort_flag, kDevTimeoutTmaEmpty, 2, (int)n, tok);
+          if (!ok) return;
+          mbar_arrive_expect_tx(&bars[L::bFull + s], L::kTileBytes);
+          load_seq_tile<D>(smem + L::kRing + s * L::kTileBytes, m, &bars[L::bFull + s], tok, hk);
+          ++slot;
+        };
+        for (int j = 0; j <= tiles && ok; ++j) {
+          if (j < tiles) load(&tm_k, seq0 + j * 128);
+          if (j > 0) load(&tm_v, seq0 + (j - 1) * 128);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      ++n;
+    }
+    if (lane == 0 && *abort_flag) {  // let the copies in flight land
+      if (q_loads > 0) drain_wait(&bars[L::bQFull], (q_loads - 1) & 1);
+      for (uint32_t s = slot > L::kStages ? slot - L::kStages : 0; s < slot; ++s)
+        drain_wait(&bars[L::bFull + s % L::kStages], (s / L::kStages) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------------------------------------------ issuer
+    regs_dec<kPrRegsLow>();
+    constexpr uint32_t idesc_qk = idesc_seq<E>(128, 128, 0, 0);
+    constexpr uint32_t idesc_pv = idesc_seq<E>(128, D, 0, 1);
+    const uint64_t qdesc = smem_desc_sw128(smem_u32(smem + L::kQ), 16, 1024);
+    const uint64_t kdesc = smem_desc_sw128(smem_u32(smem + L::kRing), 16, 1024);
+    const uint64_t vdesc = smem_desc_sw128(smem_u32(smem + L::kRing), L::kBlock, 1024);
+    int4 it;
+    uint32_t n = 0, slot = 0, np[2] = {0, 0};
+    bool ok = true;
+    const auto full = [&](uint32_t s, int site) {
+      ok = ok && warp_wait(&bars[L::bFull + s % L::kStages], (s / L::kStages) & 1, abort_flag, kDevTimeoutMma, site, (int)n, (int)s);
+      return ok;
+    };
+    const auto qk = [&](int h, uint32_t s) {
+      if (elect_one()) {
+        const uint64_t kd = kdesc + (uint64_t)(((s % L::kStages) * L::kTileBytes) >> 4);
+        const uint64_t qd = qdesc + (uint64_t)((h * L::kTileBytes) >> 4);
+        #pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4;
+          umma_ss(tmem + h * 128, qd + off, kd + off, idesc_qk, kk > 0);
+        }
+        umma_commit(&bars[L::bS + h]);
+      }
+      __syncwarp();
+    };
+    const auto pv = [&](int h, uint32_t s, bool first, bool last) {
+      ok = ok && warp_wait(&bars[L::bP + h], np[h] & 1, abort_flag, kDevTimeoutMma, 12 + h, (int)n, (int)s);
+      if (!ok) return;
+      ++np[h];
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t vd = vdesc + (uint64_t)(((s % L::kStages) * L::kTileBytes) >> 4);
+        #pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_ts(tmem + 256 + h * D, tmem + h * 128 + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv,
+                  (!first || kk > 0) ? 1u : 0u);
+        if (last) umma_commit(&bars[L::bO + h]);
+      }
+      __syncwarp();
+    };
+    const auto commit = [&](uint64_t* bar) {
+      if (elect_one()) umma_commit(bar);
+      __syncwarp();
+    };
+    while (ok && next_item(&it, 41)) {
+      const bool two = it.y > 128;
+      const int nA = it.z + 1, nB = two ? it.z + 2 : 0;
+      const int tiles = two ? nB : nA;
+      const int len = it.z * 128 + it.y;  // the sequence's tokens up to its end
+      ok = ok && warp_wait(&bars[L::bQFull], n & 1, abort_flag, kDevTimeoutMma, 10, (int)n);
+      // Ring order: K0, K1, V0, K2, V1, ..., V(tiles-1)
+      const uint32_t base = slot;
+      const auto kslot = [&](int j) { return base + (j == 0 ? 0u : 2u * j - 1u); };
+      const auto vslot = [&](int j) { return base + (j == tiles - 1 ? 2u * tiles - 1u : 2u * j + 2u); };
+      if (!full(kslot(0), 11)) break;
+      qk(0, kslot(0));
+      if (two) qk(1, kslot(0));
+      commit(&bars[L::bEmpty + kslot(0) % L::kStages]);
+      for (int j = 0; j < tiles && ok; ++j) {
+        if (!full(vslot(j), 14)) break;
+        if (len < (j + 1) * 128) clear_rows<D>(smem + L::kRing + (vslot(j) % L::kStages) * L::kTileBytes, len - j * 128);
+        if (j < nA) pv(0, vslot(j), j == 0, j == nA - 1);
+        if (j + 1 < tiles && !full(kslot(j + 1), 15)) break;
+        if (j + 1 < nA) qk(0, kslot(j + 1));
+        if (j < nB) pv(1, vslot(j), j == 0, j == nB - 1);
+        commit(&bars[L::bEmpty + vslot(j) % L::kStages]);
+        if (j + 1 < nB) qk(1, kslot(j + 1));
+        if (j + 1 < tiles) commit(&bars[L::bEmpty + kslot(j + 1) % L::kStages]);
+        if (j == tiles - 2) commit(&bars[L::bQEmpty]);  // the last product with Q has been issued
+      }
+      if (tiles == 1) commit(&bars[L::bQEmpty]);
+      slot = base + 2 * tiles;
+      ++n;
+    }
+    if (__any_sync(0xffffffffu, *abort_flag)) {  // let the products in flight end
+      commit(&bars[L::bDrain]);
+      drain_wait(&bars[L::bDrain], 0);
+      __syncwarp();
+    }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------------ item finder
+    regs_dec<kPrRegsLow>();
+    TileList list;
+    const long long total = list.init(p.seq_start, p.n_seq, p.n_tok, 256) * p.q_heads;
+    if (blockIdx.x == 0) {  // offsets that decrease or reach outside leave their sequence out: say so
+      for (int s = lane; s < p.n_seq; s += 32) {
+        const int a = __ldg(p.seq_start + s), b = __ldg(p.seq_start + s + 1);
+        if (a < 0 || b < a || b > p.n_tok) record_bad_index(kSiteSeqStart, s, a, b);
+      }
+    }
+    uint32_t n = 0;
+    for (int r = 0;; ++r) {
+      const long long x = deal(r, blockIdx.x, gridDim.x);
+      int4 it = make_int4(0, 0, 0, 0);
+      const bool more = x < total;
+      if (more) {
+        int lv;
+        const int s = list.find(x / p.q_heads, &lv);
+        int first, len;
+        seq_range(p.seq_start, p.n_tok, s, &first, &len);
+        it = make_int4(first + lv * 256, len - lv * 256, lv * 2, (int)(x % p.q_heads));
+      } else if ((long long)r * gridDim.x < total) {
+        continue;  // a round that is not full: none for this block
+      }
+      const uint32_t s = n % kPrItems;
+      if (!warp_wait(&bars[L::bItemEmpty + s], ((n / kPrItems) & 1) ^ 1, abort_flag, kDevTimeoutOther, 3, (int)n)) break;
+      if (lane == 0) {
+        items[s] = it;
+        mbar_arrive(&bars[L::bItemFull + s]);
+      }
+      __syncwarp();
+      ++n;
+      if (!more) break;
+    }
+  } else if (warp == 11) {
+    regs_dec<kPrRegsLow>();
+  } else {
+    // ------------------------------------------------------------------ softmax + epilogue
+    regs_inc<kPrRegsHigh>();
+    const int half = warp >> 2;
+    const int row = threadIdx.x & 127;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_tm = tmem + lane_base + half * 128;
+    const uint32_t o_tm = tmem + lane_base + 256 + half * D;
+    uint32_t ns = 0, no = 0;
+    int4 it;
+    while (next_item(&it, 42 + half)) {
+      if (half == 1 && it.y <= 128) continue;  // no tile B
+      const int tiles = it.z + 1 + half;
+      const bool valid = half * 128 + row < it.y;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < tiles; ++j) {
+        if (!warp_wait(&bars[L::bS + half], ns & 1, abort_flag, kDevTimeoutSoftmax, 20 + half, (int)ns, j)) goto done;
+        ++ns;
+        tc_fence_after();
+        uint32_t s[4][32];
+        #pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + c * 32, s[c]);
+        tmem_wait_ld();
+        if (j == tiles - 1) {  // the diagonal tile: key c is kept by row r iff c <= r
+          #pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c > row) s[c >> 5][c & 31] = 0xff800000u;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        #pragma unroll
+        for (int c = 0; c < 128; c += 8)
+          #pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx[e] = fmax3(mx[e], __uint_as_float(s[c >> 5][(c & 31) + 2 * e]), __uint_as_float(s[c >> 5][(c & 31) + 2 * e + 1]));
+        const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
+        const bool grow = top > m + kPrRescale || (m == -INFINITY && top > m);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float m_new = fmaxf(m, top);
+          const float a = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
+          m = m_new;
+          l *= a;
+          if (j > 0) {  // this tile's S was issued behind the last P V: O is at rest
+            #pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t ov[32];
+              tmem_ld32(o_tm + c * 32, ov);
+              tmem_wait_ld();
+              #pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * a);
+              tmem_st32(o_tm + c * 32, ov);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        const uint64_t sc2 = f32x2_pack(p.scale_log2, p.scale_log2), nb2 = f32x2_pack(-base, -base);
+        uint64_t sum[2] = {0, 0};
+        #pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
+          #pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint64_t x = f32x2_fma(f32x2_pack(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])), sc2, nb2);
+            const float p0 = ex2_approx(f32x2_lo(x)), p1 = ex2_approx(f32x2_hi(x));
+            sum[e & 1] = f32x2_add(sum[e & 1], f32x2_pack(p0, p1));
+            w[e] = E::pack(p0, p1);
+          }
+          tmem_st16(s_tm + c * 16, w);
+        }
+        sum[0] = f32x2_add(sum[0], sum[1]);
+        l += f32x2_lo(sum[0]) + f32x2_hi(sum[0]);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars[L::bP + half]);
+      }
+      // ---- epilogue
+      if (!warp_wait(&bars[L::bO + half], no & 1, abort_flag, kDevTimeoutSoftmax, 24 + half, (int)no)) goto done;
+      ++no;
+      tc_fence_after();
+      {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const long long tok = (long long)it.x + half * 128 + row;
+        T* dst = static_cast<T*>(p.o.ptr) + it.w * p.o.sh + tok * p.o.st;
+        #pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t ov[32];
+          tmem_ld32(o_tm + c * 32, ov);
+          tmem_wait_ld();
+          if (valid) {
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+              #pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[i] = E::pack(__uint_as_float(ov[8 * e + 2 * i]) * inv, __uint_as_float(ov[8 * e + 2 * i + 1]) * inv);
+              reinterpret_cast<uint4*>(dst)[c * 4 + e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        if (valid && p.lse) p.lse[(long long)it.w * p.n_tok + tok] = (m + log2f(l)) * 0.69314718055994530942f;
+      }
+      tc_fence_before();  // before the next item's first P: its P V overwrites O
+    }
+  done:;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace clear

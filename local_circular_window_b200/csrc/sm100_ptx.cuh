@@ -18,6 +18,7 @@ enum DeviceError : int {
   kDevTimeoutMma = 3,
   kDevTimeoutSoftmax = 4,
   kDevTimeoutOther = 5,
+  kDevBadIndex = 16,  // an index held in device memory was out of range and was skipped
 };
 
 // Defined once per library (single translation unit).
