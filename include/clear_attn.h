@@ -499,6 +499,26 @@ CLEAR_API clear_status_t clear_attn_prompt_fwd(const clear_seq_params_t* params,
                                                const clear_seq_view_t* v, const clear_seq_view_t* o, float* lse,
                                                void* stream);
 
+/* Workspace bytes of clear_attn_prompt_bwd (two fp32 per query row and head). */
+CLEAR_API size_t clear_attn_prompt_bwd_workspace_size(const clear_seq_params_t* params, clear_status_t* status);
+
+/*
+ * Gradients of clear_attn_prompt_fwd with respect to q, k and v, given its o and lse and the upstream
+ * gradient dO: D = rowsum(dO o), dS = P (dO V^T - D), dV = P^T dO, dK = dS^T Q / sqrt(d), dQ = dS K / sqrt(d),
+ * dK and dV summed over the query heads that share them.
+ *   q, o, dO, dq [q_heads, n_tok, d]; k, v, dk, dv [kv_heads, n_tok, d]; lse fp32 [q_heads, n_tok]
+ *   workspace: clear_attn_prompt_bwd_workspace_size bytes, 256-byte aligned; contents undefined on return
+ * Gradients are written once, in a fixed order of sums: the same call gives the same bits. Rows behind
+ * the last sequence are left as they are. As in the forward, sequences do not touch each other, and a
+ * NaN within one sequence may reach rows of its own 128-token block before it.
+ */
+CLEAR_API clear_status_t clear_attn_prompt_bwd(const clear_seq_params_t* params, const int* seq_start,
+                                               const clear_seq_view_t* q, const clear_seq_view_t* k,
+                                               const clear_seq_view_t* v, const clear_seq_view_t* o, const float* lse,
+                                               const clear_seq_view_t* dO, const clear_seq_view_t* dq,
+                                               const clear_seq_view_t* dk, const clear_seq_view_t* dv, void* workspace,
+                                               size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------------------------------------
  * Host-only scheduler queries (no GPU needed). They expose the tile enumeration the kernels use,
  * so its coverage can be checked against a brute-force mask on the CPU.

@@ -53,6 +53,11 @@ _lib.clear_attn_decode.argtypes = [_PP, _PC, _vp, _PV, _PV, _vp, _vp, ctypes.c_s
 _lib.clear_attn_prompt_fwd.restype = _i
 _lib.clear_attn_prompt_fwd.argtypes = [_PP, _vp, _PV, _PV, _PV, _PV, _vp, _vp]
 
+_lib.clear_attn_prompt_bwd_workspace_size.restype = ctypes.c_size_t
+_lib.clear_attn_prompt_bwd_workspace_size.argtypes = [_PP, ctypes.POINTER(_i)]
+_lib.clear_attn_prompt_bwd.restype = _i
+_lib.clear_attn_prompt_bwd.argtypes = [_PP, _vp, _PV, _PV, _PV, _PV, _vp, _PV, _PV, _PV, _PV, _vp, ctypes.c_size_t, _vp]
+
 
 def _view(t):
     s = t.stride()
@@ -253,5 +258,34 @@ def clear_attn_prompt_fwd(q, k, v, seq_start, o=None, lse=None, stream=None):
         if st != CLEAR_OK:
             raise ClearError(st, "clear_attn_prompt_fwd")
         return out, ls
+
+    return _run(device, stream, body)
+
+
+def prompt_bwd_workspace_size(n_tok: int, q_heads: int, kv_heads: int, d: int) -> int:
+    """Bytes of clear_attn_prompt_bwd's workspace."""
+    return _size(_lib.clear_attn_prompt_bwd_workspace_size, ClearSeqParams(1, n_tok, q_heads, kv_heads, d, 0))
+
+
+def clear_attn_prompt_bwd(q, k, v, o, lse, dO, seq_start, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Gradients of clear_attn_prompt_fwd with respect to q, k and v, given its o and lse and the upstream
+    gradient dO; those of k and v are summed over the query heads that share them. Returns (dq, dk, dv)."""
+    params = _packed(q, k, v, seq_start)
+    device, dtype = q.device, q.dtype
+    _require("o", o, q.shape, dtype, device)
+    _require("dO", dO, q.shape, dtype, device)
+    _require_dense("lse", lse, q.shape[:2], torch.float32, device)
+
+    def body(handle):
+        out = [torch.empty_like(x) if y is None else y for x, y in ((q, dq), (k, dk), (v, dv))]
+        for name, y, x in (("dq", out[0], q), ("dk", out[1], k), ("dv", out[2], v)):
+            _require(name, y, x.shape, dtype, device)
+        ws = _workspace(workspace, 0 if workspace is not None else _size(_lib.clear_attn_prompt_bwd_workspace_size, params), device)
+        st = _lib.clear_attn_prompt_bwd(params, seq_start.data_ptr(), _view(q), _view(k), _view(v), _view(o), lse.data_ptr(),
+                                        _view(dO), _view(out[0]), _view(out[1]), _view(out[2]), ws.data_ptr(),
+                                        ws.numel() * ws.element_size(), handle)
+        if st != CLEAR_OK:
+            raise ClearError(st, "clear_attn_prompt_bwd")
+        return tuple(out)
 
     return _run(device, stream, body)

@@ -5,6 +5,7 @@
 #include "clear_seq_append.cuh"
 #include "clear_seq_decode.cuh"
 #include "clear_seq_prompt.cuh"
+#include "clear_seq_prompt_bwd.cuh"
 
 namespace {
 
@@ -151,6 +152,30 @@ clear_status_t launch_prompt_fwd(const clear_seq_params_t* sp, const SeqView& q,
   return cudaGetLastError() == cudaSuccess ? CLEAR_OK : CLEAR_ERR_CUDA;
 }
 
+template <typename E, int D>
+clear_status_t launch_prompt_bwd(const clear_seq_params_t* sp, const SeqView& q, const SeqView& k, const SeqView& v, const SeqView& g,
+                                 const SeqView& dq, const SeqView& dk, const SeqView& dv, const SeqStatsParams& st, SeqBwdParams p,
+                                 int num_sms, cudaStream_t stream) {
+  using L = PromptBwdLayout<D>;
+  CUtensorMap mq, mk, mv, mg;
+  if (!make_seq_map(&mq, q, sp->q_heads, sp->n_tok, D, sp->dtype) || !make_seq_map(&mk, k, sp->kv_heads, sp->n_tok, D, sp->dtype) ||
+      !make_seq_map(&mv, v, sp->kv_heads, sp->n_tok, D, sp->dtype) || !make_seq_map(&mg, g, sp->q_heads, sp->n_tok, D, sp->dtype))
+    return CLEAR_ERR_CUDA;
+  if (cudaFuncSetAttribute(clear_seq_prompt_bwd_kernel<E, D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess ||
+      cudaFuncSetAttribute(clear_seq_prompt_bwd_kernel<E, D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
+    return CLEAR_ERR_CUDA;
+  const long long lanes = (long long)sp->n_tok * sp->q_heads * (D / 8);
+  clear_seq_bwd_stats_kernel<E, D><<<(unsigned)((lanes + kStatsThreads - 1) / kStatsThreads), kStatsThreads, 0, stream>>>(st);
+  if (cudaGetLastError() != cudaSuccess) return CLEAR_ERR_CUDA;
+  p.out1 = dv;
+  p.out2 = dk;
+  clear_seq_prompt_bwd_kernel<E, D, true><<<prompt_blocks(sp, 128, sp->kv_heads, num_sms), kPrThreads, L::kAlloc, stream>>>(mk, mv, mq, mg, p);
+  if (cudaGetLastError() != cudaSuccess) return CLEAR_ERR_CUDA;
+  p.out2 = dq;
+  clear_seq_prompt_bwd_kernel<E, D, false><<<prompt_blocks(sp, 128, sp->q_heads, num_sms), kPrThreads, L::kAlloc, stream>>>(mq, mg, mk, mv, p);
+  return cudaGetLastError() == cudaSuccess ? CLEAR_OK : CLEAR_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -266,6 +291,56 @@ clear_status_t clear_attn_prompt_fwd(const clear_seq_params_t* params, const int
                            : launch_prompt_fwd<Bf16, 128>(params, vq, vk, vv, p, num_sms, s);
   return params->d == 64 ? launch_prompt_fwd<Fp16, 64>(params, vq, vk, vv, p, num_sms, s)
                          : launch_prompt_fwd<Fp16, 128>(params, vq, vk, vv, p, num_sms, s);
+}
+
+size_t clear_attn_prompt_bwd_workspace_size(const clear_seq_params_t* params, clear_status_t* status) {
+  const clear_status_t st = check_seq_params(params);
+  if (status) *status = st;
+  return st == CLEAR_OK ? align256((size_t)params->q_heads * params->n_tok * sizeof(float2)) : 0;
+}
+
+clear_status_t clear_attn_prompt_bwd(const clear_seq_params_t* params, const int* seq_start, const clear_seq_view_t* q,
+                                     const clear_seq_view_t* k, const clear_seq_view_t* v, const clear_seq_view_t* o,
+                                     const float* lse, const clear_seq_view_t* dO, const clear_seq_view_t* dq,
+                                     const clear_seq_view_t* dk, const clear_seq_view_t* dv, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  clear_status_t st = check_seq_params(params);
+  if (st != CLEAR_OK) return st;
+  if (!seq_start || !lse) return CLEAR_ERR_INVALID_ARG;
+  const clear_seq_view_t* views[8] = {q, k, v, o, dO, dq, dk, dv};
+  SeqView w[8];
+  for (int i = 0; i < 8; ++i) {
+    const bool kv = i == 1 || i == 2 || i == 6 || i == 7;
+    if ((st = check_seq_view(views[i], kv ? params->kv_heads : params->q_heads, params->n_tok, params->d, &w[i])) != CLEAR_OK) return st;
+  }
+  if (!workspace || workspace_bytes < clear_attn_prompt_bwd_workspace_size(params, nullptr) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return CLEAR_ERR_WORKSPACE;
+  // The row statistics take one thread per 8 elements of o; their grid must fit.
+  if ((long long)params->n_tok * params->q_heads * (params->d / 8) / kStatsThreads >= INT_MAX) return CLEAR_ERR_UNSUPPORTED;
+  int num_sms = 0;
+  if ((st = check_device(&num_sms)) != CLEAR_OK) return st;
+  SeqStatsParams sp{};
+  sp.o = w[3];
+  sp.g = w[4];
+  sp.lse = lse;
+  sp.stats = static_cast<float2*>(workspace);
+  SeqBwdParams p{};
+  p.stats = sp.stats;
+  p.seq_start = sp.seq_start = seq_start;
+  p.n_seq = sp.n_seq = params->n_seq;
+  p.n_tok = sp.n_tok = params->n_tok;
+  p.q_heads = sp.q_heads = params->q_heads;
+  p.kv_heads = params->kv_heads;
+  p.group = params->q_heads / params->kv_heads;
+  p.scale = (float)(1.0 / std::sqrt((double)params->d));
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)params->d));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (params->dtype == CLEAR_DTYPE_BF16)
+    return params->d == 64 ? launch_prompt_bwd<Bf16, 64>(params, w[0], w[1], w[2], w[4], w[5], w[6], w[7], sp, p, num_sms, s)
+                           : launch_prompt_bwd<Bf16, 128>(params, w[0], w[1], w[2], w[4], w[5], w[6], w[7], sp, p, num_sms, s);
+  return params->d == 64 ? launch_prompt_bwd<Fp16, 64>(params, w[0], w[1], w[2], w[4], w[5], w[6], w[7], sp, p, num_sms, s)
+                         : launch_prompt_bwd<Fp16, 128>(params, w[0], w[1], w[2], w[4], w[5], w[6], w[7], sp, p, num_sms, s);
 }
 
 }  // extern "C"

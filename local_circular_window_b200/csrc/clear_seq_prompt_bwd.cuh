@@ -1,0 +1,484 @@
+// Causal attention over packed prompts with grouped heads: the gradients.
+//
+//   P = e^(S - lse), S = Q K^T / sqrt(d);  D_i = sum dO_i o_i;  dP = dO V^T;  dS = P (dP - D);
+//   dV = P^T dO,  dK = dS^T Q / sqrt(d), both summed over the query heads of the group;  dQ = dS K / sqrt(d).
+//
+// Three launches, deterministic, without atomics:
+//   stats   (-lse log2 e, -D) of every row, one pass over o and dO (bound by memory)
+//   kv      one item per 128-key tile and kv head: K and V stay, the group's Q and dO stream past
+//   q       one item per 128-row query tile and query head: Q and dO stay, K and V stream past
+// S and dP are computed in both, seven products in place of five: the price of writing every gradient
+// once, in a fixed order. (Adding dQ up with atomics would need 64 KB of fp32 traffic per tile and
+// would change the result from run to run; grouped heads' dK and dV add up in TMEM.)
+//
+// Both are one kernel. X1, X2 are the tiles that stay, Y1, Y2 the ones that stream (128 rows each,
+// used as halves of 64 rows):
+//            X1  X2   Y1  Y2    scores (rows = X)   acc1 +=     acc2 +=
+//   kv       K   V    Q   dO    S^T, dP^T           P^T Y2      dS^T Y1
+//   q        Q   dO   K   V     S,   dP                         dS Y1
+// Per half h: S_h = X1 Y1_h^T and dP_h = X2 Y2_h^T into TMEM; a warpgroup of its own turns them into
+// P and dS, rounded to the element type over the scores (two values a column); the accumulating
+// products read them from TMEM. One half's products run while the other half's warpgroup computes.
+//   warps 0-3 / 4-7  half 0 / 1: a thread owns one row of X and 64 columns
+//   warp 8 TMA, warp 9 products, warp 10 items, warp 11 the streamed rows' statistics (kv)
+// Rounding P and dS costs half a step of each, of random sign; sums, statistics and accumulators are fp32.
+//
+// Bound by the tensor cores: a 128 x 128 pair of tiles costs 4 (kv) or 3 (q) products of 512 cycles at
+// d = 128, next to 1024 cycles of exponentials.
+//
+// Streamed rows behind the sequence's end are cleared in shared memory before use, and their
+// columns of P and dS set to zero: what they hold, NaN included, does not count.
+#pragma once
+#include "clear_seq_prompt.cuh"
+
+namespace clear {
+
+struct SeqBwdParams {
+  SeqView out1, out2;    // kv: dv, dk; q: -, dq
+  const float2* stats;   // [q_heads, n_tok]: (-lse log2 e, -D)
+  const int* seq_start;
+  int n_seq, n_tok, q_heads, kv_heads, group;
+  float scale, scale_log2;
+};
+
+struct SeqStatsParams {
+  SeqView o, g;
+  const float* lse;
+  float2* stats;
+  const int* seq_start;
+  int n_seq, n_tok, q_heads;
+};
+
+constexpr int kStatsThreads = 256;
+
+// D / 8 lanes take one row of o and dO.
+template <typename E, int D>
+__global__ void __launch_bounds__(kStatsThreads) clear_seq_bwd_stats_kernel(const __grid_constant__ SeqStatsParams p) {
+  using T = typename E::type;
+  constexpr int kLanes = D / 8;
+  const int lane = threadIdx.x % kLanes;
+  const long long row = ((long long)blockIdx.x * kStatsThreads + threadIdx.x) / kLanes;  // token-major: heads are next to each other
+  const long long t = row / p.q_heads;
+  const int h = (int)(row - t * p.q_heads);
+  int end = __ldg(p.seq_start + p.n_seq);
+  end = end < p.n_tok ? end : p.n_tok;
+  const bool in = t < end;
+  float sum = 0.f;
+  if (in) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.o.ptr) + h * p.o.sh + t * p.o.st) + lane);
+    const uint4 b = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.g.ptr) + h * p.g.sh + t * p.g.st) + lane);
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+    #pragma unroll
+    for (int e = 0; e < 4; ++e) sum = fmaf(E::hi(x[e]), E::hi(y[e]), fmaf(E::lo(x[e]), E::lo(y[e]), sum));
+  }
+  #pragma unroll
+  for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if (in && lane == 0) {
+    const float l = __ldg(p.lse + (long long)h * p.n_tok + t);
+    // A row without a finite score (lse -inf) has P = 0: 2^(-inf) instead of 2^(-inf + inf).
+    p.stats[(long long)h * p.n_tok + t] = make_float2(l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f, -sum);
+  }
+}
+
+template <int D>
+struct PromptBwdLayout {
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kBlock = 128 * 128;
+  static constexpr int kStages = D == 128 ? 2 : 4;        // pairs (Y1, Y2)
+  static constexpr int kX = 0;
+  static constexpr int kY = kX + 2 * kTileBytes;
+  static constexpr int kStats = kY + kStages * 2 * kTileBytes;  // float2[kStages][128]
+  static constexpr int kBars = kStats + kStages * 128 * 8;
+  static constexpr int bXFull = 0, bXEmpty = 1;
+  static constexpr int bYFull = 2, bYEmpty = bYFull + kStages;
+  static constexpr int bStFull = bYEmpty + kStages, bStEmpty = bStFull + kStages;
+  static constexpr int bS = bStEmpty + kStages;           // + half: S and dP written
+  static constexpr int bP = bS + 2;                       // + half: P and dS written
+  static constexpr int bAcc = bP + 2;                     // the item's last accumulating product done
+  static constexpr int bAccFree = bAcc + 1;               // the accumulators have been read
+  static constexpr int bItemFull = bAccFree + 1, bItemEmpty = bItemFull + kPrItems;
+  static constexpr int bDrain = bItemEmpty + kPrItems;
+  static constexpr int kNumBars = bDrain + 1;
+  static constexpr int kItems = (kBars + kNumBars * 8 + 15) & ~15;
+  static constexpr int kMisc = kItems + kPrItems * 16;
+  static constexpr int kAlloc = kMisc + 16 + 1024;
+  static_assert(kAlloc <= 232448, "shared memory");
+};
+
+// An item as the ring carries it: {the sequence's first token, its length (0: end of the list), X tile, head}.
+template <typename E, int D, bool kKv>
+__global__ void __launch_bounds__(kPrThreads, 1)
+clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_x2,
+                            const __grid_constant__ CUtensorMap tm_y1, const __grid_constant__ CUtensorMap tm_y2,
+                            const __grid_constant__ SeqBwdParams p) {
+  using L = PromptBwdLayout<D>;
+  using T = typename E::type;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  int4* items = reinterpret_cast<int4*>(smem + L::kItems);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars[L::bXFull], 1);
+    mbar_init(&bars[L::bXEmpty], 1);
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&bars[L::bYFull + s], 1);
+      mbar_init(&bars[L::bYEmpty + s], 1);
+      mbar_init(&bars[L::bStFull + s], 32);
+      mbar_init(&bars[L::bStEmpty + s], 8);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&bars[L::bS + h], 1);
+      mbar_init(&bars[L::bP + h], 128);
+    }
+    mbar_init(&bars[L::bAcc], 1);
+    mbar_init(&bars[L::bAccFree], 256);
+    for (int i = 0; i < kPrItems; ++i) {
+      mbar_init(&bars[L::bItemFull + i], 1);
+      mbar_init(&bars[L::bItemEmpty + i], 10 + (kKv ? 1 : 0));  // loader, issuer, eight softmax warps, statistics
+    }
+    mbar_init(&bars[L::bDrain], 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  uint32_t n_item = 0;
+  const auto next_item = [&](int4* it, int site) -> bool {
+    const uint32_t s = n_item % kPrItems;
+    if (!warp_wait(&bars[L::bItemFull + s], (n_item / kPrItems) & 1, abort_flag, kDevTimeoutOther, site, (int)n_item)) return false;
+    *it = items[s];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[L::bItemEmpty + s]);
+    ++n_item;
+    return it->y > 0;
+  };
+  // Streamed tiles of an item: kv: for each head of the group the query tiles from the key tile on;
+  // q: the key tiles up to the query tile.
+  const auto n_tiles = [](const int4& it) { return (it.y + 127) >> 7; };
+  const auto steps_of = [&](const int4& it) { return kKv ? p.group * (n_tiles(it) - it.z) : it.z + 1; };
+
+  if (warp == 8) {
+    // ------------------------------------------------------------------ loader
+    regs_dec<kPrRegsLow>();
+    int4 it;
+    uint32_t n = 0, slot = 0, x_loads = 0;
+    bool ok = true;
+    while (ok && next_item(&it, 50)) {
+      if (lane == 0) {
+        const int steps = steps_of(it), per = kKv ? n_tiles(it) - it.z : steps;
+        ok = mbar_wait(&bars[L::bXEmpty], (n & 1) ^ 1, abort_flag, kDevTimeoutTmaEmpty, 1, (int)n);
+        if (ok) {
+          mbar_arrive_expect_tx(&bars[L::bXFull], 2 * L::kTileBytes);
+          load_seq_tile<D>(smem + L::kX, &tm_x1, &bars[L::bXFull], it.x + it.z * 128, it.w);
+          load_seq_tile<D>(smem + L::kX + L::kTileBytes, &tm_x2, &bars[L::bXFull], it.x + it.z * 128, it.w);
+          ++x_loads;
+        }
+        for (int i = 0; i < steps && ok; ++i) {
+          const uint32_t s = slot % L::kStages;
+          ok = mbar_wait(&bars[L::bYEmpty + s], ((slot / L::kStages) & 1) ^ 1, abort_flag, kDevTimeoutTmaEmpty, 2, (int)n, i);
+          if (!ok) break;
+          const int tile = kKv ? it.z + i % per : i;
+          const int head = kKv ? it.w * p.group + i / per : it.w / p.group;
+          uint8_t* dst = smem + L::kY + s * 2 * L::kTileBytes;
+          mbar_arrive_expect_tx(&bars[L::bYFull + s], 2 * L::kTileBytes);
+          load_seq_tile<D>(dst, &tm_y1, &bars[L::bYFull + s], it.x + tile * 128, head);
+          load_seq_tile<D>(dst + L::kTileBytes, &tm_y2, &bars[L::bYFull + s], it.x + tile * 128, head);
+          ++slot;
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      ++n;
+    }
+    if (lane == 0 && *abort_flag) {  // let the copies in flight land
+      if (x_loads > 0) drain_wait(&bars[L::bXFull], (x_loads - 1) & 1);
+      for (uint32_t s = slot > L::kStages ? slot - L::kStages : 0; s < slot; ++s)
+        drain_wait(&bars[L::bYFull + s % L::kStages], (s / L::kStages) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------------------------------------------ issuer
+    regs_dec<kPrRegsLow>();
+    constexpr uint32_t idesc_s = idesc_seq<E>(128, 64, 0, 0);
+    constexpr uint32_t idesc_a = idesc_seq<E>(128, D, 0, 1);
+    const uint64_t xdesc = smem_desc_sw128(smem_u32(smem + L::kX), 16, 1024);
+    const uint64_t ykdesc = smem_desc_sw128(smem_u32(smem + L::kY), 16, 1024);         // as K-major B operand
+    const uint64_t ymdesc = smem_desc_sw128(smem_u32(smem + L::kY), L::kBlock, 1024);  // as MN-major B operand
+    int4 it;
+    uint32_t n = 0, slot = 0, np[2] = {0, 0};
+    bool ok = true;
+    // S_h and dP_h of the streamed pair in slot s
+    const auto scores = [&](int h, uint32_t s) {
+      if (elect_one()) {
+        const uint64_t yd = ykdesc + (uint64_t)(((s % L::kStages) * 2 * L::kTileBytes + h * 8192) >> 4);
+        #pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          #pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4;
+            umma_ss(tmem + x * 128 + h * 64, xdesc + ((x * L::kTileBytes) >> 4) + off, yd + ((x * L::kTileBytes) >> 4) + off,
+                    idesc_s, kk > 0);
+          }
+        }
+        umma_commit(&bars[L::bS + h]);
+      }
+      __syncwarp();
+    };
+    const auto accumulate = [&](int h, uint32_t s, bool first) {
+      ok = ok && warp_wait(&bars[L::bP + h], np[h] & 1, abort_flag, kDevTimeoutMma, 12 + h, (int)n, (int)s);
+      if (!ok) return;
+      ++np[h];
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t yd = ymdesc + (uint64_t)(((s % L::kStages) * 2 * L::kTileBytes + h * 8192) >> 4);
+        if (kKv) {
+          #pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_ts(tmem + 256, tmem + h * 64 + kk * 8, yd + ((L::kTileBytes + kk * 2048) >> 4), idesc_a, (!first || kk > 0) ? 1u : 0u);
+        }
+        #pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_ts(tmem + 256 + D, tmem + 128 + h * 64 + kk * 8, yd + ((kk * 2048) >> 4), idesc_a, (!first || kk > 0) ? 1u : 0u);
+      }
+      __syncwarp();
+    };
+    const auto commit = [&](uint64_t* bar) {
+      if (elect_one()) umma_commit(bar);
+      __syncwarp();
+    };
+    while (ok && next_item(&it, 51)) {
+      const int steps = steps_of(it), per = kKv ? n_tiles(it) - it.z : steps;
+      // The streamed pair of step i has landed, and rows behind the sequence's end are cleared.
+      const auto ready = [&](int i) -> bool {
+        const uint32_t s = slot + i;
+        ok = ok && warp_wait(&bars[L::bYFull + s % L::kStages], (s / L::kStages) & 1, abort_flag, kDevTimeoutMma, 11, (int)n, i);
+        if (!ok) return false;
+        const int left = it.y - (kKv ? it.z + i % per : i) * 128;
+        if (left < 128) {
+          uint8_t* y = smem + L::kY + (s % L::kStages) * 2 * L::kTileBytes;
+          clear_rows<D>(y, left);
+          clear_rows<D>(y + L::kTileBytes, left);
+        }
+        return true;
+      };
+      ok = ok && warp_wait(&bars[L::bXFull], n & 1, abort_flag, kDevTimeoutMma, 10, (int)n);
+      if (!ready(0)) break;
+      scores(0, slot);
+      scores(1, slot);
+      if (steps == 1) commit(&bars[L::bXEmpty]);
+      // The accumulators are free once the previous item's have been written out.
+      ok = ok && warp_wait(&bars[L::bAccFree], (n & 1) ^ 1, abort_flag, kDevTimeoutMma, 14, (int)n);
+      for (int i = 0; i < steps && ok; ++i) {
+        accumulate(0, slot + i, i == 0);
+        if (i + 1 < steps) {
+          if (!ready(i + 1)) break;
+          scores(0, slot + i + 1);
+        }
+        accumulate(1, slot + i, false);
+        commit(&bars[L::bYEmpty + (slot + i) % L::kStages]);
+        if (i + 1 < steps) scores(1, slot + i + 1);
+        if (i == steps - 2) commit(&bars[L::bXEmpty]);
+      }
+      if (!ok) break;
+      commit(&bars[L::bAcc]);
+      slot += steps;
+      ++n;
+    }
+    if (__any_sync(0xffffffffu, *abort_flag)) {  // let the products in flight end
+      commit(&bars[L::bDrain]);
+      drain_wait(&bars[L::bDrain], 0);
+      __syncwarp();
+    }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------------ item finder
+    regs_dec<kPrRegsLow>();
+    TileList list;
+    const int heads = kKv ? p.kv_heads : p.q_heads;
+    const long long total = list.init(p.seq_start, p.n_seq, p.n_tok, 128) * heads;
+    if (kKv && blockIdx.x == 0) {
+      for (int s = lane; s < p.n_seq; s += 32) {
+        const int a = __ldg(p.seq_start + s), b = __ldg(p.seq_start + s + 1);
+        if (a < 0 || b < a || b > p.n_tok) record_bad_index(kSiteSeqStart, s, a, b);
+      }
+    }
+    uint32_t n = 0;
+    for (int r = 0;; ++r) {
+      const long long x = deal(r, blockIdx.x, gridDim.x);
+      int4 it = make_int4(0, 0, 0, 0);
+      const bool more = x < total;
+      if (more) {
+        int lv;  // steps: level + 1 query tiles (kv: those from the key tile on) or key tiles (q)
+        const int s = list.find(x / heads, &lv);
+        int first, len;
+        seq_range(p.seq_start, p.n_tok, s, &first, &len);
+        it = make_int4(first, len, kKv ? ((len + 127) >> 7) - 1 - lv : lv, (int)(x % heads));
+      } else if ((long long)r * gridDim.x < total) {
+        continue;
+      }
+      const uint32_t s = n % kPrItems;
+      if (!warp_wait(&bars[L::bItemEmpty + s], ((n / kPrItems) & 1) ^ 1, abort_flag, kDevTimeoutOther, 3, (int)n)) break;
+      if (lane == 0) {
+        items[s] = it;
+        mbar_arrive(&bars[L::bItemFull + s]);
+      }
+      __syncwarp();
+      ++n;
+      if (!more) break;
+    }
+  } else if (warp == 11) {
+    // ------------------------------------------------------------------ statistics of streamed rows
+    regs_dec<kPrRegsLow>();
+    if constexpr (kKv) {
+      float2* ring = reinterpret_cast<float2*>(smem + L::kStats);
+      int4 it;
+      uint32_t slot = 0;
+      bool ok = true;
+      while (ok && next_item(&it, 52)) {
+        const int steps = steps_of(it), per = n_tiles(it) - it.z;
+        for (int i = 0; i < steps; ++i, ++slot) {
+          const int t0 = (it.z + i % per) * 128;
+          const float2* src = p.stats + (long long)(it.w * p.group + i / per) * p.n_tok + it.x + t0;
+          float2 v[4];
+          #pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = t0 + e * 32 + lane < it.y ? src[e * 32 + lane] : make_float2(0.f, 0.f);
+          const uint32_t s = slot % L::kStages;
+          ok = warp_wait(&bars[L::bStEmpty + s], ((slot / L::kStages) & 1) ^ 1, abort_flag, kDevTimeoutOther, 4, (int)slot);
+          if (!ok) break;
+          #pragma unroll
+          for (int e = 0; e < 4; ++e) ring[s * 128 + e * 32 + lane] = v[e];
+          mbar_arrive(&bars[L::bStFull + s]);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ P, dS and the epilogue
+    regs_inc<kPrRegsHigh>();
+    const int half = warp >> 2;
+    const int row = threadIdx.x & 127;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_tm = tmem + lane_base + half * 64;
+    const uint32_t d_tm = s_tm + 128;
+    const uint64_t sc2 = f32x2_pack(p.scale_log2, p.scale_log2);
+    const float4* stats = reinterpret_cast<const float4*>(smem + L::kStats);
+    uint32_t ns = 0, n = 0, slot = 0;
+    int4 it;
+    while (next_item(&it, 53 + half)) {
+      const int steps = steps_of(it), per = kKv ? n_tiles(it) - it.z : steps;
+      const bool valid = it.z * 128 + row < it.y;
+      const long long tok = (long long)it.x + it.z * 128 + row;
+      float2 mine = make_float2(0.f, 0.f);
+      if (!kKv && valid) mine = p.stats[(long long)it.w * p.n_tok + tok];
+      for (int i = 0; i < steps; ++i, ++slot) {
+        const int yt = kKv ? it.z + i % per : i;
+        const uint32_t st = slot % L::kStages;
+        if (kKv && !warp_wait(&bars[L::bStFull + st], (slot / L::kStages) & 1, abort_flag, kDevTimeoutSoftmax, 22 + half, (int)slot)) goto done;
+        if (!warp_wait(&bars[L::bS + half], ns & 1, abort_flag, kDevTimeoutSoftmax, 20 + half, (int)ns, i)) goto done;
+        ++ns;
+        tc_fence_after();
+        // Columns kept: kv: query c >= key row on the diagonal, inside the sequence; q: key c <= query row.
+        int lo = 0, hi = 128;
+        if (kKv) {
+          if (yt == it.z) lo = row;
+          hi = it.y - yt * 128;
+        } else if (yt == it.z) {
+          hi = row + 1;
+        }
+        lo -= half * 64;
+        hi -= half * 64;
+        const bool all = lo <= 0 && hi >= 64;
+        const bool warp_all = __all_sync(0xffffffffu, all);
+        #pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t s[32], g[32], wp[16], wd[16];
+          tmem_ld32(s_tm + c * 32, s);
+          tmem_ld32(d_tm + c * 32, g);
+          tmem_wait_ld();
+          #pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            uint64_t nl, nd;
+            if (kKv) {
+              const float4 v = stats[(st * 128 + half * 64 + c * 32 + 2 * e) >> 1];
+              nl = f32x2_pack(v.x, v.z);
+              nd = f32x2_pack(v.y, v.w);
+            } else {
+              nl = f32x2_pack(mine.x, mine.x);
+              nd = f32x2_pack(mine.y, mine.y);
+            }
+            const uint64_t x = f32x2_fma(f32x2_pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), sc2, nl);
+            float p0 = ex2_approx(f32x2_lo(x)), p1 = ex2_approx(f32x2_hi(x));
+            const uint64_t ds = f32x2_mul(f32x2_pack(p0, p1),
+                                          f32x2_add(f32x2_pack(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1])), nd));
+            float d0 = f32x2_lo(ds), d1 = f32x2_hi(ds);
+            if (!warp_all) {
+              const int col = c * 32 + 2 * e;
+              const bool k0 = col >= lo && col < hi, k1 = col + 1 >= lo && col + 1 < hi;
+              p0 = k0 ? p0 : 0.f;
+              d0 = k0 ? d0 : 0.f;
+              p1 = k1 ? p1 : 0.f;
+              d1 = k1 ? d1 : 0.f;
+            }
+            if (kKv) wp[e] = E::pack(p0, p1);
+            wd[e] = E::pack(d0, d1);
+          }
+          if (kKv) tmem_st16(s_tm + c * 16, wp);
+          tmem_st16(d_tm + c * 16, wd);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars[L::bP + half]);
+        if (kKv) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[L::bStEmpty + st]);
+        }
+      }
+      // ---- epilogue: kv: this half writes dv (0) or dk (1); q: its half of dq's columns
+      if (!warp_wait(&bars[L::bAcc], n & 1, abort_flag, kDevTimeoutSoftmax, 24 + half, (int)n)) goto done;
+      ++n;
+      tc_fence_after();
+      {
+        constexpr int kCols = kKv ? D : D / 2;
+        const bool one = kKv && half == 0;
+        const SeqView& out = one ? p.out1 : p.out2;
+        const int c0 = kKv ? 0 : half * (D / 2);
+        const uint32_t acc = tmem + lane_base + 256 + (one ? 0 : D) + c0;
+        const float f = one ? 1.f : p.scale;
+        T* dst = static_cast<T*>(out.ptr) + it.w * out.sh + tok * out.st + c0;
+        #pragma unroll
+        for (int c = 0; c < kCols / 32; ++c) {
+          uint32_t ov[32];
+          tmem_ld32(acc + c * 32, ov);
+          tmem_wait_ld();
+          if (valid) {
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+              #pragma unroll
+              for (int u = 0; u < 4; ++u)
+                w[u] = E::pack(__uint_as_float(ov[8 * e + 2 * u]) * f, __uint_as_float(ov[8 * e + 2 * u + 1]) * f);
+              reinterpret_cast<uint4*>(dst)[c * 4 + e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&bars[L::bAccFree]);
+    }
+  done:;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace clear

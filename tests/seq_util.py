@@ -79,3 +79,30 @@ def check_attention(name, o, lse, q, k, v, p_type, out_type, keep=None):
     ref, rl, av = attend(q, k, v, keep)
     check(name + " o", o, ref, (unit(p_type) + SCORE) * av + unit(out_type) * ref.abs() + tiny(out_type))
     check(name + " lse", lse, rl, torch.full_like(rl, LSE_ABS))
+
+
+def gradients(q, k, v, g):
+    """Gradients of causal attention of one head (q, k, v, g [n, d]) in 64 bits, and the error that the kernels'
+    arithmetic allows each, for element type q.dtype: ((dq, dk, dv), (tolerances)) without the final
+    rounding's part, which the caller adds once the shared heads are summed.
+
+    P: half a step when rounded, and EP relative: the score's error and that of the given lse. dP: fp32, (d + 1) roundings
+    of sum |g v|. D = sum g o from the rounded o. dS = P (dP - D): half a step when rounded, and what its
+    factors are off by. Sums in fp32 add at most 2e-5 of the sum of magnitudes."""
+    u, d = unit(q.dtype), q.shape[1]
+    q, k, v, g = (x.double() for x in (q, k, v, g))
+    n, s = q.shape[0], 1 / math.sqrt(d)
+    keep = torch.ones(n, n, dtype=torch.bool).tril()
+    o, lse, av = attend(q, k, v, keep)
+    p = torch.exp((q @ k.T * s).masked_fill(~keep, -math.inf) - lse[:, None])
+    dp = g @ v.T
+    dd = (g * o).sum(-1, keepdim=True)
+    ds = p * (dp - dd)
+    ep = SCORE / 2 + LSE_ABS + 1e-6
+    o_err = (u + SCORE) * av + u * o.abs()
+    d_err = (g.abs() * o_err).sum(-1, keepdim=True)
+    dp_err = (d + 1) * 2.0 ** -24 * (g.abs() @ v.abs().T)
+    ds_err = (u + ep) * ds.abs() + p * (dp_err + d_err) * (1 + u + ep)
+    more = 2e-5
+    tol = (s * ((ds_err + more * ds.abs()) @ k.abs()), s * ((ds_err + more * ds.abs()).T @ q.abs()), (u + ep + more) * (p.T @ g.abs()))
+    return (s * (ds @ k), s * (ds.T @ q), p.T @ g), tol

@@ -62,12 +62,18 @@ def prompt(p=None, ss=PTR, q="same", k="same", v="same", o="same", lse=PTR):
     return LIB.clear_attn_prompt_fwd(p or params(), ss, pick(q), pick(k), pick(v), pick(o), lse, None)
 
 
+def backward(p=None, ss=PTR, lse=PTR, ws=PTR, size=1 << 30, **kw):
+    views = [kw.get(n, view()) for n in ("q", "k", "v", "o", "dO", "dq", "dk", "dv")]
+    return LIB.clear_attn_prompt_bwd(p or params(), ss, *views[:4], lse, *views[4:], ws, size, None)
+
+
 @pytest.mark.parametrize("fields,status", BAD_PARAMS)
 def test_params(fields, status):
     p = params(**fields)
-    assert append(p) == status and decode(p) == status and prompt(p) == status
+    assert append(p) == status and decode(p) == status and prompt(p) == status and backward(p) == status
     st = ctypes.c_int(0)
     assert LIB.clear_attn_decode_workspace_size(p, ctypes.byref(st)) == 0 and st.value == status
+    assert LIB.clear_attn_prompt_bwd_workspace_size(p, ctypes.byref(st)) == 0 and st.value == status
     assert LIB.clear_attn_decode(None, cache(), PTR, view(), view(), PTR, PTR, 1 << 30, None) == 1
 
 
@@ -82,6 +88,8 @@ def test_views(fields, status):
         assert decode(**{name: v}) == status
     for name in ("q", "k", "v", "o"):
         assert prompt(**{name: v}) == status
+    for name in ("q", "k", "v", "o", "dO", "dq", "dk", "dv"):
+        assert backward(**{name: v}) == status
 
 
 @pytest.mark.parametrize("fields,status", BAD_CACHES)
@@ -97,6 +105,9 @@ def test_indexes_workspace_and_queries():
     assert append(ss=None) == 1 and append(sl=None) == 1 and append(qo=None) == 1 and append(q=None) == 1
     assert decode(sl=None) == 1 and decode(p=params(n_tok=3)) == 1 and prompt(ss=None) == 1
     need = L.decode_workspace_size(2, 4, 2, 64)
+    assert backward(ss=None) == 1 and backward(lse=None) == 1
+    size = L.prompt_bwd_workspace_size(2, 4, 2, 64)
+    assert backward(ws=None) == 3 and backward(size=size - 1) == 3 and backward(ws=PTR + 16) == 3
     assert decode(ws=None) == 3 and decode(size=need - 1) == 3 and decode(ws=PTR + 16) == 3
 
 
