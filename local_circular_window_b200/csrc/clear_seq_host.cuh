@@ -167,12 +167,12 @@ clear_status_t launch_prompt_bwd(const clear_seq_params_t* sp, const SeqView& q,
   const long long lanes = (long long)sp->n_tok * sp->q_heads * (D / 8);
   clear_seq_bwd_stats_kernel<E, D><<<(unsigned)((lanes + kStatsThreads - 1) / kStatsThreads), kStatsThreads, 0, stream>>>(st);
   if (cudaGetLastError() != cudaSuccess) return CLEAR_ERR_CUDA;
+  p.out2 = dq;  // first: it settles the first rows' statistics for the other
+  clear_seq_prompt_bwd_kernel<E, D, false><<<prompt_blocks(sp, 128, sp->q_heads, num_sms), kPrThreads, L::kAlloc, stream>>>(mq, mg, mk, mv, p);
+  if (cudaGetLastError() != cudaSuccess) return CLEAR_ERR_CUDA;
   p.out1 = dv;
   p.out2 = dk;
   clear_seq_prompt_bwd_kernel<E, D, true><<<prompt_blocks(sp, 128, sp->kv_heads, num_sms), kPrThreads, L::kAlloc, stream>>>(mk, mv, mq, mg, p);
-  if (cudaGetLastError() != cudaSuccess) return CLEAR_ERR_CUDA;
-  p.out2 = dq;
-  clear_seq_prompt_bwd_kernel<E, D, false><<<prompt_blocks(sp, 128, sp->q_heads, num_sms), kPrThreads, L::kAlloc, stream>>>(mq, mg, mk, mv, p);
   return cudaGetLastError() == cudaSuccess ? CLEAR_OK : CLEAR_ERR_CUDA;
 }
 
