@@ -34,6 +34,19 @@ __device__ __noinline__ void record_bad_index(int site, int c0, int c1, int c2) 
   }
 }
 
+// mbar_wait for a whole warp: every lane returns the same, so that a warp leaves its loop together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int err_code, int site,
+                                          int c0 = 0, int c1 = 0) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err_code, site, c0, c1));
+}
+
+// After an expired wait: waits, again with a limit, for a copy or product still in flight, whatever
+// the abort flag says, so that nothing writes shared or tensor memory after the block has left.
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_test(bar, parity) && globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(100);
+}
+
 // 16-bit element types: one pair per 32-bit register, the lower half first.
 struct Bf16 {
   using type = __nv_bfloat16;

@@ -80,8 +80,6 @@ clear_status_t launch_append_d(const SeqAppendParams& a, int d, bool halves, cud
 }
 
 // ---------------------------------------------------------------------------------------- decode
-// Blocks of the decode grid: two per SM, as many as are resident at once.
-constexpr int kDecMaxBlocks = 2 * 160;
 
 struct DecodeWorkspace {
   size_t ml_off, split_off, total;
@@ -94,17 +92,44 @@ DecodeWorkspace decode_workspace_layout(int d) {
   return w;
 }
 
+// A cache side as (128 bytes of a row, heads, rows, blocks of 128 bytes, pages), in boxes of 16 whole rows of one head,
+// which land block by block. Axes of one element get a stride that passes the encoder's checks.
+bool make_cache_map(CUtensorMap* m, void* base, const long long* st, const SeqCache& c, int heads, int d, int elem_bytes, int box_bytes) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  const int blocks = d * elem_bytes / box_bytes;
+  cuuint64_t dims[5] = {(cuuint64_t)(box_bytes / elem_bytes), (cuuint64_t)heads, (cuuint64_t)c.page_size, (cuuint64_t)blocks,
+                        (cuuint64_t)c.n_pages};
+  const auto bytes = [&](long long s) { return (cuuint64_t)(s > 0 ? s : d) * elem_bytes; };
+  cuuint64_t strides[4] = {bytes(st[2]), bytes(st[1]), (cuuint64_t)box_bytes, bytes(st[0])};
+  cuuint32_t box[5] = {(cuuint32_t)(box_bytes / elem_bytes), 1, (cuuint32_t)kDecSlice, (cuuint32_t)blocks, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return enc(m, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, base, dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             d * elem_bytes >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename E, bool kF8, int D>
-clear_status_t launch_decode(const SeqDecodeParams& p, int num_sms, cudaStream_t stream) {
-  using L = DecLayout<kF8, D>;
-  if (cudaFuncSetAttribute(clear_seq_decode_kernel<E, kF8, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem) != cudaSuccess)
+clear_status_t launch_decode(SeqDecodeParams p, int num_sms, cudaStream_t stream) {
+  using L1 = DecLayout<kF8, D, 1>;
+  using L2 = DecLayout<kF8, D, 2>;
+  CUtensorMap mk{}, mv{};
+  p.tma = p.c.page_size % kDecSlice == 0;
+  if (p.tma && (!make_cache_map(&mk, p.c.k, p.c.ks, p.c, p.kv_heads, D, kF8 ? 1 : 2, L1::kBox) ||
+                !make_cache_map(&mv, p.c.v, p.c.vs, p.c, p.kv_heads, D, kF8 ? 1 : 2, L1::kBox)))
     return CLEAR_ERR_CUDA;
-  const int blocks = 2 * num_sms < kDecMaxBlocks ? 2 * num_sms : kDecMaxBlocks;
-  clear_seq_decode_kernel<E, kF8, D><<<blocks, kDecThreads, L::kSmem, stream>>>(p);
+  // Up to eight heads of a group fill one tile of the matrix instruction, more take two.
+  const auto kernel = p.group <= 8 ? clear_seq_decode_kernel<E, kF8, D, 1> : clear_seq_decode_kernel<E, kF8, D, 2>;
+  const int smem = p.group <= 8 ? L1::kSmem : L2::kSmem;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return CLEAR_ERR_CUDA;
+  const int blocks = kDecPerSm * num_sms < kDecMaxBlocks ? kDecPerSm * num_sms : kDecMaxBlocks;
+  kernel<<<blocks, kDecThreads, smem, stream>>>(mk, mv, p);
   if (cudaGetLastError() != cudaSuccess) return CLEAR_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(blocks, p.group < kDecRows ? p.group : kDecRows);
-  cfg.blockDim = dim3(D);
+  cfg.blockDim = dim3(kJoinParts * D);
   cfg.stream = stream;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -167,19 +167,6 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int from) {
   __syncwarp();
 }
 
-// mbar_wait for a whole warp: every lane returns the same, so that a warp leaves its loop together.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int err_code, int site,
-                                          int c0 = 0, int c1 = 0) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err_code, site, c0, c1));
-}
-
-// After an expired wait: waits, again with a limit, for a copy or product still in flight, whatever
-// the abort flag says, so that nothing writes shared or tensor memory after the block has left.
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_test(bar, parity) && globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(100);
-}
-
 // An item as the ring carries it: {first token of tile A, query rows left from there, tile A's number, head}.
 template <typename E, int D>
 __global__ void __launch_bounds__(kPrThreads, 1)
