@@ -28,7 +28,9 @@ def __getattr__(name):
     if name in _EXPORTS:
         return getattr(importlib.import_module("._binding", __name__), name)
     if name in _SEQUENCE_EXPORTS:
-        return getattr(importlib.import_module("._sequence", __name__), name)
+        value = getattr(importlib.import_module("._sequence", __name__), name)
+        globals()[name] = value  # the next access does not come here
+        return value
     raise AttributeError(name)
 
 

@@ -2,12 +2,25 @@
 // tensor maps and launches. Included by clear_attn.cu.
 #pragma once
 
+#include <atomic>
+
 #include "clear_seq_append.cuh"
 #include "clear_seq_decode.cuh"
 #include "clear_seq_prompt.cuh"
 #include "clear_seq_prompt_bwd.cuh"
 
 namespace {
+
+// Allows a kernel `bytes` of dynamic shared memory, once per device: `done` has a bit for each of the first 64.
+bool allow_smem(const void* kernel, int bytes, std::atomic<unsigned long long>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (done->load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  done->fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
 
 bool seq_strides_ok(long long s, long long per16, long long n) {
   // A stride that is used (more than one element along its axis) is a positive multiple of 16 bytes.
@@ -122,8 +135,8 @@ clear_status_t launch_decode(SeqDecodeParams p, int num_sms, cudaStream_t stream
   // Up to eight heads of a group fill one tile of the matrix instruction, more take two.
   const auto kernel = p.group <= 8 ? clear_seq_decode_kernel<E, kF8, D, 1> : clear_seq_decode_kernel<E, kF8, D, 2>;
   const int smem = p.group <= 8 ? L1::kSmem : L2::kSmem;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return CLEAR_ERR_CUDA;
+  static std::atomic<unsigned long long> done[2];
+  if (!allow_smem(reinterpret_cast<const void*>(kernel), smem, &done[p.group <= 8 ? 0 : 1])) return CLEAR_ERR_CUDA;
   const int blocks = kDecPerSm * num_sms < kDecMaxBlocks ? kDecPerSm * num_sms : kDecMaxBlocks;
   kernel<<<blocks, kDecThreads, smem, stream>>>(mk, mv, p);
   if (cudaGetLastError() != cudaSuccess) return CLEAR_ERR_CUDA;
@@ -171,8 +184,8 @@ clear_status_t launch_prompt_fwd(const clear_seq_params_t* sp, const SeqView& q,
   if (!make_seq_map(&mq, q, sp->q_heads, sp->n_tok, D, sp->dtype) || !make_seq_map(&mk, k, sp->kv_heads, sp->n_tok, D, sp->dtype) ||
       !make_seq_map(&mv, v, sp->kv_heads, sp->n_tok, D, sp->dtype))
     return CLEAR_ERR_CUDA;
-  if (cudaFuncSetAttribute(clear_seq_prompt_fwd_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
-    return CLEAR_ERR_CUDA;
+  static std::atomic<unsigned long long> done;
+  if (!allow_smem(reinterpret_cast<const void*>(clear_seq_prompt_fwd_kernel<E, D>), L::kAlloc, &done)) return CLEAR_ERR_CUDA;
   clear_seq_prompt_fwd_kernel<E, D><<<prompt_blocks(sp, 256, sp->q_heads, num_sms), kPrThreads, L::kAlloc, stream>>>(mq, mk, mv, p);
   return cudaGetLastError() == cudaSuccess ? CLEAR_OK : CLEAR_ERR_CUDA;
 }
@@ -186,8 +199,9 @@ clear_status_t launch_prompt_bwd(const clear_seq_params_t* sp, const SeqView& q,
   if (!make_seq_map(&mq, q, sp->q_heads, sp->n_tok, D, sp->dtype) || !make_seq_map(&mk, k, sp->kv_heads, sp->n_tok, D, sp->dtype) ||
       !make_seq_map(&mv, v, sp->kv_heads, sp->n_tok, D, sp->dtype) || !make_seq_map(&mg, g, sp->q_heads, sp->n_tok, D, sp->dtype))
     return CLEAR_ERR_CUDA;
-  if (cudaFuncSetAttribute(clear_seq_prompt_bwd_kernel<E, D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess ||
-      cudaFuncSetAttribute(clear_seq_prompt_bwd_kernel<E, D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
+  static std::atomic<unsigned long long> done[2];
+  if (!allow_smem(reinterpret_cast<const void*>(clear_seq_prompt_bwd_kernel<E, D, true>), L::kAlloc, &done[0]) ||
+      !allow_smem(reinterpret_cast<const void*>(clear_seq_prompt_bwd_kernel<E, D, false>), L::kAlloc, &done[1]))
     return CLEAR_ERR_CUDA;
   const long long lanes = (long long)sp->n_tok * sp->q_heads * (D / 8);
   clear_seq_bwd_stats_kernel<E, D><<<(unsigned)((lanes + kStatsThreads - 1) / kStatsThreads), kStatsThreads, 0, stream>>>(st);

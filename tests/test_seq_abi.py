@@ -9,7 +9,15 @@ import torch
 import local_circular_window_b200 as L
 from local_circular_window_b200 import _sequence as S
 
-LIB = L.lib()
+class ByReference:
+    """The library with structures passed by reference."""
+
+    def __getattr__(self, name):
+        f = getattr(L.lib(), name)
+        return lambda *a: f(*(ctypes.byref(x) if isinstance(x, ctypes.Structure) else x for x in a))
+
+
+LIB = ByReference()
 BUF = np.full(1 << 16, 0x5A, dtype=np.uint8)
 PTR = (BUF.ctypes.data + 255) & ~255
 OK = dict(n_seq=2, n_tok=2, q_heads=4, kv_heads=2, d=64, dtype=0)
