@@ -34,10 +34,37 @@ __device__ __noinline__ void record_bad_index(int site, int c0, int c1, int c2) 
   }
 }
 
-// mbar_wait for a whole warp: every lane returns the same, so that a warp leaves its loop together.
+// A bounded wait like mbar_wait, for waits that are short and many: the timer, a slow read, is first looked at
+// after some polls.
+__device__ __forceinline__ bool seq_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int err_code, int site,
+                                         int c0 = 0, int c1 = 0) {
+  const uint32_t a = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (uint32_t spins = 1;; ++spins) {
+    if (mbar_try_wait(a, parity)) return true;
+    if ((spins & 63u) == 0) {
+      if (*abort_flag) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) {
+        record_timeout(abort_flag, err_code, site, (int)parity, c0, c1, (int)(a & 0xffff));
+        return false;
+      }
+    }
+  }
+}
+
+// The same for a whole warp: every lane returns the same, so that a warp leaves its loop together.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int err_code, int site,
                                           int c0 = 0, int c1 = 0) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err_code, site, c0, c1));
+  return __all_sync(0xffffffffu, seq_wait(bar, parity, abort_flag, err_code, site, c0, c1));
+}
+
+// One arrival for the whole warp, behind its tensor-memory accesses so far (which the caller has waited for).
+__device__ __forceinline__ void warp_arrive_tc(uint64_t* bar) {
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 // After an expired wait: waits, again with a limit, for a copy or product still in flight, whatever

@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecPerSm) clear_seq_decode_kerne
 
     for (int i = 0; i < mine; ++i) {
       const uint32_t s = reads % L::kStages;
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars[s], (reads / L::kStages) & 1, give_up, kDevTimeoutTmaFull, 36, seq, i));
+      ok = ok && warp_wait(&bars[s], (reads / L::kStages) & 1, give_up, kDevTimeoutTmaFull, 36, seq, i);
       if (!ok) break;
       const uint32_t ks = ring_u + s * L::kSliceBytes;
       const uint32_t vs = ks + L::kSide;

@@ -13,7 +13,8 @@
 //   warp 8           TMA: Q tiles, then K and V tiles through one ring (K0 K1 V0 K2 V1 ...)
 //   warp 9           issues the products: S = Q K^T into TMEM, then O += P V with P from TMEM
 //   warp 10          finds the block's items, ahead of the others, through a small ring
-// TMEM: S of A and B at columns 0 and 128 (P overwrites S, 16-bit, two values a column), O at 256 and 256 + d.
+// TMEM: S of A and B at columns 0 and 128 (P overwrites S, 16-bit, two values a column: the 32 keys of each
+// 32 columns go into the first 16), O at 256 and 256 + d.
 // While one tile's softmax runs, the other tile's products do: the issuer alternates A, B.
 //
 // Items are ordered by their number of key tiles, the longest first, over all sequences, and dealt to
@@ -40,6 +41,7 @@ constexpr uint32_t kPrRegsLow = 88, kPrRegsHigh = 208;
 static_assert(2 * 128 * kPrRegsHigh + 128 * kPrRegsLow <= 384 * 168, "register split exceeds the launch allocation");
 constexpr int kPrItems = 4;  // item ring
 constexpr float kPrRescale = 8.0f;
+constexpr int kPrParts = 2;  // P is handed to its product in halves of 64 keys
 
 struct SeqPromptParams {
   SeqView o;
@@ -121,6 +123,17 @@ __device__ __forceinline__ long long deal(int r, int block, int blocks) {
   return (long long)r * blocks + ((r & 1) ? blocks - 1 - block : block);
 }
 
+// Waits for this thread's loads from tensor memory; x is not used before it.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&x)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]), "+r"(x[8]),
+                 "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15]), "+r"(x[16]),
+                 "+r"(x[17]), "+r"(x[18]), "+r"(x[19]), "+r"(x[20]), "+r"(x[21]), "+r"(x[22]), "+r"(x[23]), "+r"(x[24]),
+                 "+r"(x[25]), "+r"(x[26]), "+r"(x[27]), "+r"(x[28]), "+r"(x[29]), "+r"(x[30]), "+r"(x[31])
+               :
+               : "memory");
+}
+
 template <int D>
 struct PromptLayout {
   static constexpr int kTileBytes = 128 * D * 2;
@@ -132,8 +145,8 @@ struct PromptLayout {
   static constexpr int bQFull = 0, bQEmpty = 1;
   static constexpr int bFull = 2, bEmpty = bFull + kStages;
   static constexpr int bS = bEmpty + kStages;            // + tile: S written
-  static constexpr int bP = bS + 2;                      // + tile: P written (and O rescaled)
-  static constexpr int bO = bP + 2;                      // + tile: the item's last P V done
+  static constexpr int bP = bS + 2;                      // + tile * kPrParts + part: P's part written (and O rescaled)
+  static constexpr int bO = bP + 2 * kPrParts;           // + tile: the item's last P V done
   static constexpr int bItemFull = bO + 2, bItemEmpty = bItemFull + kPrItems;
   static constexpr int bDrain = bItemEmpty + kPrItems;
   static constexpr int kNumBars = bDrain + 1;
@@ -191,7 +204,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
     }
     for (int h = 0; h < 2; ++h) {
       mbar_init(&bars[L::bS + h], 1);
-      mbar_init(&bars[L::bP + h], 128);
+      for (int i = 0; i < kPrParts; ++i) mbar_init(&bars[L::bP + h * kPrParts + i], 4);
       mbar_init(&bars[L::bO + h], 1);
     }
     for (int i = 0; i < kPrItems; ++i) {
@@ -235,7 +248,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
         const bool two = it.y > 128;
         const int tiles = it.z + (two ? 2 : 1);  // key tiles of the item
         const int seq0 = it.x - it.z * 128;      // the sequence's first token
-        ok = mbar_wait(&bars[L::bQEmpty], (n & 1) ^ 1, abort_flag, kDevTimeoutTmaEmpty, 1, (int)n);
+        ok = seq_wait(&bars[L::bQEmpty], (n & 1) ^ 1, abort_flag, kDevTimeoutTmaEmpty, 1, (int)n);
         if (ok) {
           mbar_arrive_expect_tx(&bars[L::bQFull], (two ? 2 : 1) * L::kTileBytes);
           load_seq_tile<D>(smem + L::kQ, &tm_q, &bars[L::bQFull], it.x, it.w);
@@ -244,7 +257,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
         }
         const auto load = [&](const CUtensorMap* m, int tok) {
           const uint32_t s = slot % L::kStages;
-          ok = ok && mbar_wait(&bars[L::bEmpty + s], ((slot / L::kStages) & 1) ^ 1, abort_flag, kDevTimeoutTmaEmpty, 2, (int)n, tok);
+          ok = ok && seq_wait(&bars[L::bEmpty + s], ((slot / L::kStages) & 1) ^ 1, abort_flag, kDevTimeoutTmaEmpty, 2, (int)n, tok);
           if (!ok) return;
           mbar_arrive_expect_tx(&bars[L::bFull + s], L::kTileBytes);
           load_seq_tile<D>(smem + L::kRing + s * L::kTileBytes, m, &bars[L::bFull + s], tok, hk);
@@ -293,19 +306,22 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
       __syncwarp();
     };
     const auto pv = [&](int h, uint32_t s, bool first, bool last) {
-      ok = ok && warp_wait(&bars[L::bP + h], np[h] & 1, abort_flag, kDevTimeoutMma, 12 + h, (int)n, (int)s);
-      if (!ok) return;
-      ++np[h];
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t vd = vdesc + (uint64_t)(((s % L::kStages) * L::kTileBytes) >> 4);
-        #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_ts(tmem + 256 + h * D, tmem + h * 128 + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv,
-                  (!first || kk > 0) ? 1u : 0u);
-        if (last) umma_commit(&bars[L::bO + h]);
+      #pragma unroll
+      for (int i = 0; i < kPrParts; ++i) {
+        ok = ok && warp_wait(&bars[L::bP + h * kPrParts + i], np[h] & 1, abort_flag, kDevTimeoutMma, 12 + h, (int)n, (int)s);
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t vd = vdesc + (uint64_t)(((s % L::kStages) * L::kTileBytes) >> 4);
+          #pragma unroll
+          for (int kk = i * (8 / kPrParts); kk < (i + 1) * (8 / kPrParts); ++kk)
+            umma_ts(tmem + 256 + h * D, tmem + h * 128 + (kk >> 1) * 32 + (kk & 1) * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv,
+                    (!first || kk > 0) ? 1u : 0u);
+          if (last && i == kPrParts - 1) umma_commit(&bars[L::bO + h]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
+      ++np[h];
     };
     const auto commit = [&](uint64_t* bar) {
       if (elect_one()) umma_commit(bar);
@@ -402,21 +418,57 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
         if (!warp_wait(&bars[L::bS + half], ns & 1, abort_flag, kDevTimeoutSoftmax, 20 + half, (int)ns, j)) goto done;
         ++ns;
         tc_fence_after();
-        uint32_t s[4][32];
-        #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + c * 32, s[c]);
-        tmem_wait_ld();
-        if (j == tiles - 1) {  // the diagonal tile: key c is kept by row r iff c <= r
+        // The exponentials of the first 64 keys are taken with the maximum in use while the true maximum of all 128 is
+        // still being found: the comparisons run in the special-function unit's shadow. Only where the
+        // maximum has to move are they taken again.
+        const bool diagonal = j == tiles - 1;  // key c is kept by row r iff c <= r
+        uint32_t a0[32], a1[32], a2[32], a3[32], w0[16], w1[16];
+        tmem_ld32(s_tm, a0);
+        tmem_ld32(s_tm + 32, a1);
+        tmem_ld32(s_tm + 64, a2);
+        tmem_ld32(s_tm + 96, a3);
+        tmem_wait_ld(a0);
+        tmem_wait_ld(a1);
+        tmem_wait_ld(a2);
+        tmem_wait_ld(a3);
+        const auto cut = [&](uint32_t (&x)[32], int c0) {
+          if (diagonal) {
+            #pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c0 + e > row) x[e] = 0xff800000u;
+          }
+        };
+        cut(a0, 0);
+        cut(a1, 32);
+        cut(a2, 64);
+        cut(a3, 96);
+        const uint64_t sc2 = f32x2_pack(p.scale_log2, p.scale_log2);
+        uint64_t sum[2] = {0, 0};
+        const auto probabilities = [&](const uint32_t (&x)[32], float base, uint32_t (&w)[16]) {
+          const uint64_t nb2 = f32x2_pack(-base, -base);
           #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c > row) s[c >> 5][c & 31] = 0xff800000u;
-        }
+          for (int e = 0; e < 16; ++e) {
+            const uint64_t y = f32x2_fma(f32x2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc2, nb2);
+            const float p0 = ex2_approx(f32x2_lo(y)), p1 = ex2_approx(f32x2_hi(y));
+            sum[e & 1] = f32x2_add(sum[e & 1], f32x2_pack(p0, p1));
+            w[e] = E::pack(p0, p1);
+          }
+        };
+        float base = m == -INFINITY ? 0.f : m;
+        probabilities(a0, base, w0);
+        probabilities(a1, base, w1);
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        #pragma unroll
-        for (int c = 0; c < 128; c += 8)
+        const auto largest = [&](const uint32_t (&x)[32]) {
           #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mx[e] = fmax3(mx[e], __uint_as_float(s[c >> 5][(c & 31) + 2 * e]), __uint_as_float(s[c >> 5][(c & 31) + 2 * e + 1]));
+          for (int e = 0; e < 32; e += 2) {
+            float& y = mx[(e >> 1) & 3];
+            y = fmax3(y, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+          }
+        };
+        largest(a0);
+        largest(a1);
+        largest(a2);
+        largest(a3);
         const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
         const bool grow = top > m + kPrRescale || (m == -INFINITY && top > m);
         if (__any_sync(0xffffffffu, grow)) {
@@ -427,35 +479,38 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
           if (j > 0) {  // this tile's S was issued behind the last P V: O is at rest
             #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
-              uint32_t ov[32];
-              tmem_ld32(o_tm + c * 32, ov);
-              tmem_wait_ld();
+              tmem_ld32(o_tm + c * 32, a0);
+              tmem_wait_ld(a0);
               #pragma unroll
-              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * a);
-              tmem_st32(o_tm + c * 32, ov);
+              for (int e = 0; e < 32; ++e) a0[e] = __float_as_uint(__uint_as_float(a0[e]) * a);
+              tmem_st32(o_tm + c * 32, a0);
             }
           }
+          tmem_ld32(s_tm, a0);
+          tmem_ld32(s_tm + 32, a1);
+          tmem_wait_ld(a0);
+          tmem_wait_ld(a1);
+          cut(a0, 0);
+          cut(a1, 32);
+          sum[0] = sum[1] = 0;
+          base = m == -INFINITY ? 0.f : m;
+          probabilities(a0, base, w0);
+          probabilities(a1, base, w1);
         }
-        const float base = m == -INFINITY ? 0.f : m;
-        const uint64_t sc2 = f32x2_pack(p.scale_log2, p.scale_log2), nb2 = f32x2_pack(-base, -base);
-        uint64_t sum[2] = {0, 0};
-        #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
-          #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint64_t x = f32x2_fma(f32x2_pack(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])), sc2, nb2);
-            const float p0 = ex2_approx(f32x2_lo(x)), p1 = ex2_approx(f32x2_hi(x));
-            sum[e & 1] = f32x2_add(sum[e & 1], f32x2_pack(p0, p1));
-            w[e] = E::pack(p0, p1);
-          }
-          tmem_st16(s_tm + c * 16, w);
-        }
+        const auto hand_over = [&](int part) {
+          tmem_wait_st();
+          warp_arrive_tc(&bars[L::bP + half * kPrParts + part]);
+        };
+        tmem_st16(s_tm, w0);
+        tmem_st16(s_tm + 32, w1);
+        hand_over(0);
+        probabilities(a2, base, w0);
+        tmem_st16(s_tm + 64, w0);
+        probabilities(a3, base, w1);
+        tmem_st16(s_tm + 96, w1);
+        hand_over(1);
         sum[0] = f32x2_add(sum[0], sum[1]);
         l += f32x2_lo(sum[0]) + f32x2_hi(sum[0]);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&bars[L::bP + half]);
       }
       // ---- epilogue
       if (!warp_wait(&bars[L::bO + half], no & 1, abort_flag, kDevTimeoutSoftmax, 24 + half, (int)no)) goto done;

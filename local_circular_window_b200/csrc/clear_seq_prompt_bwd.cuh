@@ -139,10 +139,10 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
     }
     for (int h = 0; h < 2; ++h) {
       mbar_init(&bars[L::bS + h], 1);
-      mbar_init(&bars[L::bP + h], 128);
+      mbar_init(&bars[L::bP + h], 4);
     }
     mbar_init(&bars[L::bAcc], 1);
-    mbar_init(&bars[L::bAccFree], 256);
+    mbar_init(&bars[L::bAccFree], 8);
     mbar_init(&bars[L::bD], 256);
     for (int i = 0; i < kPrItems; ++i) {
       mbar_init(&bars[L::bItemFull + i], 1);
@@ -185,7 +185,7 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
     while (ok && next_item(&it, 50)) {
       if (lane == 0) {
         const int steps = steps_of(it), per = kKv ? n_tiles(it) - it.z : steps;
-        ok = mbar_wait(&bars[L::bXEmpty], (n & 1) ^ 1, abort_flag, kDevTimeoutTmaEmpty, 1, (int)n);
+        ok = seq_wait(&bars[L::bXEmpty], (n & 1) ^ 1, abort_flag, kDevTimeoutTmaEmpty, 1, (int)n);
         if (ok) {
           mbar_arrive_expect_tx(&bars[L::bXFull], 2 * L::kTileBytes);
           load_seq_tile<D>(smem + L::kX, &tm_x1, &bars[L::bXFull], it.x + it.z * 128, it.w);
@@ -194,7 +194,7 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
         }
         for (int i = 0; i < steps && ok; ++i) {
           const uint32_t s = slot % L::kStages;
-          ok = mbar_wait(&bars[L::bYEmpty + s], ((slot / L::kStages) & 1) ^ 1, abort_flag, kDevTimeoutTmaEmpty, 2, (int)n, i);
+          ok = seq_wait(&bars[L::bYEmpty + s], ((slot / L::kStages) & 1) ^ 1, abort_flag, kDevTimeoutTmaEmpty, 2, (int)n, i);
           if (!ok) break;
           const int tile = kKv ? it.z + i % per : i;
           const int head = kKv ? it.w * p.group + i / per : it.w / p.group;
@@ -462,12 +462,8 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
           tmem_st16(d_tm + c * 16, wd);
         }
         tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&bars[L::bP + half]);
-        if (kKv) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[L::bStEmpty + st]);
-        }
+        warp_arrive_tc(&bars[L::bP + half]);
+        if (kKv && lane == 0) mbar_arrive(&bars[L::bStEmpty + st]);
       }
       // ---- epilogue: kv: this half writes dv (0) or dk (1); q: its half of dq's columns
       if (!warp_wait(&bars[L::bAcc], n & 1, abort_flag, kDevTimeoutSoftmax, 24 + half, (int)n)) goto done;
@@ -498,8 +494,7 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
           }
         }
       }
-      tc_fence_before();
-      mbar_arrive(&bars[L::bAccFree]);
+      warp_arrive_tc(&bars[L::bAccFree]);
     }
   done:;
   }
