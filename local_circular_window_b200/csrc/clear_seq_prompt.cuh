@@ -11,11 +11,12 @@
 // head of one sequence; each key/value tile of 128 is loaded once for both.
 //   warps 0-3 / 4-7  softmax and epilogue of tile A / B; a thread owns one row (= one TMEM lane)
 //   warp 8           TMA: Q tiles, then K and V tiles through one ring (K0 K1 V0 K2 V1 ...)
-//   warp 9           issues the products: S = Q K^T into TMEM, then O += P V with P from TMEM
-//   warp 10          finds the block's items, ahead of the others, through a small ring
+//   warp 9           one thread issues the products: S = Q K^T into TMEM, then O += P V with P from TMEM
+//   warp 11          finds the block's items, ahead of the others, through a small ring
 // TMEM: S of A and B at columns 0 and 128 (P overwrites S, 16-bit, two values a column: the 32 keys of each
 // 32 columns go into the first 16), O at 256 and 256 + d.
-// While one tile's softmax runs, the other tile's products do: the issuer alternates A, B.
+// While one tile's softmax runs, the other tile's products do: the issuer alternates A, B. (An issuer for each
+// tile mixes the two tiles' products in the tensor pipe: 1782 us in place of 1416 at 16896 tokens and 24 heads.)
 //
 // Items are ordered by their number of key tiles, the longest first, over all sequences, and dealt to
 // the blocks back and forth, so that every block gets about the same work. Heads of one group follow
@@ -26,8 +27,8 @@
 // the second product (half a step of each probability, of random sign); sums are of the unrounded values.
 //
 // Value rows behind the sequence's end belong to the next sequence or to nothing. Their
-// probabilities are zero, but 0 * NaN is not: the issuer clears those rows in shared memory before
-// the tile that holds them is used.
+// probabilities are zero, but 0 * NaN is not: the threads of the tile that uses them (the diagonal's)
+// clear those rows in shared memory before they hand over P.
 #pragma once
 #include <type_traits>
 
@@ -286,83 +287,98 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
     const uint64_t kdesc = smem_desc_sw128(smem_u32(smem + L::kRing), 16, 1024);
     const uint64_t vdesc = smem_desc_sw128(smem_u32(smem + L::kRing), L::kBlock, 1024);
     int4 it;
-    uint32_t n = 0, slot = 0, np[2] = {0, 0};
+    uint32_t n = 0, np0 = 0, np1 = 0;
+    uint32_t stage = 0, phase = 0;  // of the next tile in the ring
     bool ok = true;
-    const auto full = [&](uint32_t s, int site) {
-      ok = ok && warp_wait(&bars[L::bFull + s % L::kStages], (s / L::kStages) & 1, abort_flag, kDevTimeoutMma, site, (int)n, (int)s);
-      return ok;
-    };
-    const auto qk = [&](int h, uint32_t s) {
-      if (elect_one()) {
-        const uint64_t kd = kdesc + (uint64_t)(((s % L::kStages) * L::kTileBytes) >> 4);
-        const uint64_t qd = qdesc + (uint64_t)((h * L::kTileBytes) >> 4);
-        #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4;
-          umma_ss(tmem + h * 128, qd + off, kd + off, idesc_qk, kk > 0);
-        }
-        umma_commit(&bars[L::bS + h]);
-      }
-      __syncwarp();
-    };
-    const auto pv = [&](int h, uint32_t s, bool first, bool last) {
-      #pragma unroll
-      for (int i = 0; i < kPrParts; ++i) {
-        ok = ok && warp_wait(&bars[L::bP + h * kPrParts + i], np[h] & 1, abort_flag, kDevTimeoutMma, 12 + h, (int)n, (int)s);
-        if (!ok) return;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t vd = vdesc + (uint64_t)(((s % L::kStages) * L::kTileBytes) >> 4);
-          #pragma unroll
-          for (int kk = i * (8 / kPrParts); kk < (i + 1) * (8 / kPrParts); ++kk)
-            umma_ts(tmem + 256 + h * D, tmem + h * 128 + (kk >> 1) * 32 + (kk & 1) * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv,
-                    (!first || kk > 0) ? 1u : 0u);
-          if (last && i == kPrParts - 1) umma_commit(&bars[L::bO + h]);
-        }
-        __syncwarp();
-      }
-      ++np[h];
-    };
-    const auto commit = [&](uint64_t* bar) {
-      if (elect_one()) umma_commit(bar);
-      __syncwarp();
-    };
     while (ok && next_item(&it, 41)) {
-      const bool two = it.y > 128;
-      const int nA = it.z + 1, nB = two ? it.z + 2 : 0;
-      const int tiles = two ? nB : nA;
-      const int len = it.z * 128 + it.y;  // the sequence's tokens up to its end
-      ok = ok && warp_wait(&bars[L::bQFull], n & 1, abort_flag, kDevTimeoutMma, 10, (int)n);
-      // Ring order: K0, K1, V0, K2, V1, ..., V(tiles-1)
-      const uint32_t base = slot;
-      const auto kslot = [&](int j) { return base + (j == 0 ? 0u : 2u * j - 1u); };
-      const auto vslot = [&](int j) { return base + (j == tiles - 1 ? 2u * tiles - 1u : 2u * j + 2u); };
-      if (!full(kslot(0), 11)) break;
-      qk(0, kslot(0));
-      if (two) qk(1, kslot(0));
-      commit(&bars[L::bEmpty + kslot(0) % L::kStages]);
-      for (int j = 0; j < tiles && ok; ++j) {
-        if (!full(vslot(j), 14)) break;
-        if (len < (j + 1) * 128) clear_rows<D>(smem + L::kRing + (vslot(j) % L::kStages) * L::kTileBytes, len - j * 128);
-        if (j < nA) pv(0, vslot(j), j == 0, j == nA - 1);
-        if (j + 1 < tiles && !full(kslot(j + 1), 15)) break;
-        if (j + 1 < nA) qk(0, kslot(j + 1));
-        if (j < nB) pv(1, vslot(j), j == 0, j == nB - 1);
-        commit(&bars[L::bEmpty + vslot(j) % L::kStages]);
-        if (j + 1 < nB) qk(1, kslot(j + 1));
-        if (j + 1 < tiles) commit(&bars[L::bEmpty + kslot(j + 1) % L::kStages]);
-        if (j == tiles - 2) commit(&bars[L::bQEmpty]);  // the last product with Q has been issued
+      if (elect_one()) {
+        const bool two = it.y > 128;
+        const int nA = it.z + 1, nB = two ? it.z + 2 : 0;
+        const int tiles = two ? nB : nA;
+        const auto advance = [&]() {
+          if (++stage == L::kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        };
+        const auto full = [&](uint32_t st, uint32_t ph) {
+          ok = ok && seq_wait(&bars[L::bFull + st], ph, abort_flag, kDevTimeoutMma, 11, (int)n, (int)st);
+        };
+        const auto qk = [&](int h, uint32_t st) {
+          const uint64_t kd = kdesc + (uint64_t)((st * L::kTileBytes) >> 4);
+          const uint64_t qd = qdesc + (uint64_t)((h * L::kTileBytes) >> 4);
+          #pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4;
+            umma_ss(tmem + h * 128, qd + off, kd + off, idesc_qk, kk > 0);
+          }
+          umma_commit(&bars[L::bS + h]);
+        };
+        const auto pv = [&](int h, uint32_t st, uint32_t ph, bool first) {
+          const uint64_t vd = vdesc + (uint64_t)((st * L::kTileBytes) >> 4);
+          #pragma unroll
+          for (int i = 0; i < kPrParts; ++i) {
+            ok = ok && seq_wait(&bars[L::bP + h * kPrParts + i], ph & 1, abort_flag, kDevTimeoutMma, 13 + h, (int)n, (int)st);
+            if (!ok) return;
+            tc_fence_after();
+            #pragma unroll
+            for (int kk = i * (8 / kPrParts); kk < (i + 1) * (8 / kPrParts); ++kk)
+              umma_ts(tmem + 256 + h * D, tmem + h * 128 + (kk >> 1) * 32 + (kk & 1) * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv,
+                      (!first || kk > 0) ? 1u : 0u);
+          }
+        };
+        ok = seq_wait(&bars[L::bQFull], n & 1, abort_flag, kDevTimeoutMma, 10, (int)n);
+        // Ring order: K0, K1, V0, K2, V1, ..., V(tiles-1)
+        full(stage, phase);
+        if (ok) {
+          qk(0, stage);
+          if (two) qk(1, stage);
+          umma_commit(&bars[L::bEmpty + stage]);
+          if (tiles == 1) umma_commit(&bars[L::bQEmpty]);
+          advance();
+        }
+        for (int j = 0; j < tiles && ok; ++j) {
+          const uint32_t kst = stage, kph = phase;
+          if (j + 1 < tiles) {
+            full(kst, kph);
+            advance();
+          }
+          full(stage, phase);
+          if (!ok) break;
+          if (j < nA) {
+            pv(0, stage, np0++, j == 0);
+            if (!ok) break;
+            if (j == nA - 1) umma_commit(&bars[L::bO]);
+            else qk(0, kst);
+          }
+          if (j < nB) {
+            pv(1, stage, np1++, j == 0);
+            if (!ok) break;
+          }
+          umma_commit(&bars[L::bEmpty + stage]);
+          if (j == nB - 1) umma_commit(&bars[L::bO + 1]);
+          if (j + 1 < nB) qk(1, kst);
+          if (j + 1 < tiles) {
+            umma_commit(&bars[L::bEmpty + kst]);
+            if (j + 2 == tiles) umma_commit(&bars[L::bQEmpty]);  // the last product with Q has been issued
+          }
+          advance();
+        }
       }
-      if (tiles == 1) commit(&bars[L::bQEmpty]);
-      slot = base + 2 * tiles;
+      __syncwarp();
+      ok = __all_sync(0xffffffffu, ok);
       ++n;
     }
     if (__any_sync(0xffffffffu, *abort_flag)) {  // let the products in flight end
-      commit(&bars[L::bDrain]);
-      drain_wait(&bars[L::bDrain], 0);
+      if (elect_one()) {
+        umma_commit(&bars[L::bDrain]);
+        drain_wait(&bars[L::bDrain], 0);
+      }
       __syncwarp();
     }
   } else if (warp == 10) {
+    regs_dec<kPrRegsLow>();
+  } else if (warp == 11) {
     // ------------------------------------------------------------------ item finder
     regs_dec<kPrRegsLow>();
     TileList list;
@@ -397,8 +413,6 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
       ++n;
       if (!more) break;
     }
-  } else if (warp == 11) {
-    regs_dec<kPrRegsLow>();
   } else {
     // ------------------------------------------------------------------ softmax + epilogue
     regs_inc<kPrRegsHigh>();
@@ -407,9 +421,12 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_tm = tmem + lane_base + half * 128;
     const uint32_t o_tm = tmem + lane_base + 256 + half * D;
-    uint32_t ns = 0, no = 0;
+    uint32_t ns = 0, no = 0, tiles_before = 0;  // key tiles of earlier items
     int4 it;
     while (next_item(&it, 42 + half)) {
+      const uint32_t ring0 = 2 * tiles_before;  // the item's first place in the ring
+      const int all_tiles = it.z + (it.y > 128 ? 2 : 1);
+      tiles_before += all_tiles;
       if (half == 1 && it.y <= 128) continue;  // no tile B
       const int tiles = it.z + 1 + half;
       const bool valid = half * 128 + row < it.y;
@@ -501,6 +518,16 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
           tmem_wait_st();
           warp_arrive_tc(&bars[L::bP + half * kPrParts + part]);
         };
+        if (diagonal && it.y < (half + 1) * 128) {  // the tile reaches behind the sequence's end: clear its value rows there
+          const uint32_t v = ring0 + (j == all_tiles - 1 ? 2 * all_tiles - 1 : 2 * j + 2), st = v % L::kStages;
+          if (!warp_wait(&bars[L::bFull + st], (v / L::kStages) & 1, abort_flag, kDevTimeoutSoftmax, 26 + half, (int)v, j)) goto done;
+          if (half * 128 + row >= it.y) {
+            uint8_t* r = smem + L::kRing + st * L::kTileBytes + row * 128;
+            #pragma unroll
+            for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(r + (c >> 3) * L::kBlock + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
         tmem_st16(s_tm, w0);
         tmem_st16(s_tm + 32, w1);
         hand_over(0);
