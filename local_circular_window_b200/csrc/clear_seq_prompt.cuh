@@ -170,17 +170,6 @@ __device__ __forceinline__ void load_seq_tile(uint8_t* dst, const CUtensorMap* m
   for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * kHalfBytes, m, bar, c * 64, tok, h);
 }
 
-// Rows [from, 128) of a 128-row tile in shared memory become zero (whole warp).
-template <int D>
-__device__ __forceinline__ void clear_rows(uint8_t* tile, int from) {
-  for (int i = threadIdx.x & 31; i < (128 - from) * (D / 8); i += 32) {
-    const int r = from + i / (D / 8), c = i % (D / 8);
-    *reinterpret_cast<uint4*>(tile + (c >> 3) * kHalfBytes + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-  }
-  fence_proxy_async_smem();
-  __syncwarp();
-}
-
 // An item as the ring carries it: {first token of tile A, query rows left from there, tile A's number, head}.
 template <typename E, int D>
 __global__ void __launch_bounds__(kPrThreads, 1)

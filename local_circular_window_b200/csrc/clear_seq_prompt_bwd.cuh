@@ -223,88 +223,81 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
     const uint64_t ykdesc = smem_desc_sw128(smem_u32(smem + L::kY), 16, 1024);         // as K-major B operand
     const uint64_t ymdesc = smem_desc_sw128(smem_u32(smem + L::kY), L::kBlock, 1024);  // as MN-major B operand
     int4 it;
-    uint32_t n = 0, slot = 0, np[2] = {0, 0};
+    uint32_t n = 0, np = 0;         // items; streamed pairs
+    uint32_t stage = 0, phase = 0;  // of the next pair in the ring
     bool ok = true;
-    // S_h and dP_h of the streamed pair in slot s
-    const auto scores = [&](int h, uint32_t s) {
+    while (ok && next_item(&it, 51)) {
       if (elect_one()) {
-        const uint64_t yd = ykdesc + (uint64_t)(((s % L::kStages) * 2 * L::kTileBytes + h * 8192) >> 4);
-        #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        const int steps = steps_of(it);
+        // S_h and dP_h of the streamed pair in stage s
+        const auto scores = [&](int h, uint32_t s) {
+          const uint64_t yd = ykdesc + (uint64_t)((s * 2 * L::kTileBytes + h * 8192) >> 4);
           #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4;
-            umma_ss(tmem + x * 128 + h * 64, xdesc + ((x * L::kTileBytes) >> 4) + off, yd + ((x * L::kTileBytes) >> 4) + off,
-                    idesc_s, kk > 0);
+          for (int x = 0; x < 2; ++x) {
+            #pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4;
+              umma_ss(tmem + x * 128 + h * 64, xdesc + ((x * L::kTileBytes) >> 4) + off, yd + ((x * L::kTileBytes) >> 4) + off,
+                      idesc_s, kk > 0);
+            }
           }
-        }
-        umma_commit(&bars[L::bS + h]);
-      }
-      __syncwarp();
-    };
-    const auto accumulate = [&](int h, uint32_t s, bool first) {
-      ok = ok && warp_wait(&bars[L::bP + h], np[h] & 1, abort_flag, kDevTimeoutMma, 12 + h, (int)n, (int)s);
-      if (!ok) return;
-      ++np[h];
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t yd = ymdesc + (uint64_t)(((s % L::kStages) * 2 * L::kTileBytes + h * 8192) >> 4);
-        if (kKv) {
+          umma_commit(&bars[L::bS + h]);
+        };
+        const auto accumulate = [&](int h, uint32_t s, bool first) {
+          ok = ok && seq_wait(&bars[L::bP + h], np & 1, abort_flag, kDevTimeoutMma, 12 + h, (int)n, (int)np);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t yd = ymdesc + (uint64_t)((s * 2 * L::kTileBytes + h * 8192) >> 4);
+          if (kKv) {
+            #pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_ts(tmem + 256, tmem + h * 64 + kk * 8, yd + ((L::kTileBytes + kk * 2048) >> 4), idesc_a, (!first || kk > 0) ? 1u : 0u);
+          }
           #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_ts(tmem + 256, tmem + h * 64 + kk * 8, yd + ((L::kTileBytes + kk * 2048) >> 4), idesc_a, (!first || kk > 0) ? 1u : 0u);
+            umma_ts(tmem + 256 + D, tmem + 128 + h * 64 + kk * 8, yd + ((kk * 2048) >> 4), idesc_a, (!first || kk > 0) ? 1u : 0u);
+        };
+        const auto ready = [&](uint32_t s, uint32_t ph, int i) {
+          ok = ok && seq_wait(&bars[L::bYFull + s], ph, abort_flag, kDevTimeoutMma, 11, (int)n, i);
+        };
+        ok = seq_wait(&bars[L::bXFull], n & 1, abort_flag, kDevTimeoutMma, 10, (int)n);
+        ready(stage, phase, 0);
+        if (ok) {
+          scores(0, stage);
+          scores(1, stage);
+          if (steps == 1) umma_commit(&bars[L::bXEmpty]);
+          // The accumulators are free once the previous item's have been written out.
+          ok = seq_wait(&bars[L::bAccFree], (n & 1) ^ 1, abort_flag, kDevTimeoutMma, 14, (int)n);
         }
-        #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_ts(tmem + 256 + D, tmem + 128 + h * 64 + kk * 8, yd + ((kk * 2048) >> 4), idesc_a, (!first || kk > 0) ? 1u : 0u);
+        for (int i = 0; i < steps && ok; ++i) {
+          const uint32_t s = stage;
+          if (++stage == L::kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+          const bool more = i + 1 < steps;
+          if (more) ready(stage, phase, i + 1);
+          accumulate(0, s, i == 0);
+          if (!ok) break;
+          if (more) scores(0, stage);
+          accumulate(1, s, false);
+          if (!ok) break;
+          ++np;
+          umma_commit(&bars[L::bYEmpty + s]);
+          if (more) scores(1, stage);
+          if (i + 2 == steps) umma_commit(&bars[L::bXEmpty]);
+        }
+        if (ok) umma_commit(&bars[L::bAcc]);
       }
       __syncwarp();
-    };
-    const auto commit = [&](uint64_t* bar) {
-      if (elect_one()) umma_commit(bar);
-      __syncwarp();
-    };
-    while (ok && next_item(&it, 51)) {
-      const int steps = steps_of(it), per = kKv ? n_tiles(it) - it.z : steps;
-      // The streamed pair of step i has landed, and rows behind the sequence's end are cleared.
-      const auto ready = [&](int i) -> bool {
-        const uint32_t s = slot + i;
-        ok = ok && warp_wait(&bars[L::bYFull + s % L::kStages], (s / L::kStages) & 1, abort_flag, kDevTimeoutMma, 11, (int)n, i);
-        if (!ok) return false;
-        const int left = it.y - (kKv ? it.z + i % per : i) * 128;
-        if (left < 128) {
-          uint8_t* y = smem + L::kY + (s % L::kStages) * 2 * L::kTileBytes;
-          clear_rows<D>(y, left);
-          clear_rows<D>(y + L::kTileBytes, left);
-        }
-        return true;
-      };
-      ok = ok && warp_wait(&bars[L::bXFull], n & 1, abort_flag, kDevTimeoutMma, 10, (int)n);
-      if (!ready(0)) break;
-      scores(0, slot);
-      scores(1, slot);
-      if (steps == 1) commit(&bars[L::bXEmpty]);
-      // The accumulators are free once the previous item's have been written out.
-      ok = ok && warp_wait(&bars[L::bAccFree], (n & 1) ^ 1, abort_flag, kDevTimeoutMma, 14, (int)n);
-      for (int i = 0; i < steps && ok; ++i) {
-        accumulate(0, slot + i, i == 0);
-        if (i + 1 < steps) {
-          if (!ready(i + 1)) break;
-          scores(0, slot + i + 1);
-        }
-        accumulate(1, slot + i, false);
-        commit(&bars[L::bYEmpty + (slot + i) % L::kStages]);
-        if (i + 1 < steps) scores(1, slot + i + 1);
-        if (i == steps - 2) commit(&bars[L::bXEmpty]);
-      }
-      if (!ok) break;
-      commit(&bars[L::bAcc]);
-      slot += steps;
+      ok = __all_sync(0xffffffffu, ok);
       ++n;
     }
     if (__any_sync(0xffffffffu, *abort_flag)) {  // let the products in flight end
-      commit(&bars[L::bDrain]);
-      drain_wait(&bars[L::bDrain], 0);
+      if (elect_one()) {
+        umma_commit(&bars[L::bDrain]);
+        drain_wait(&bars[L::bDrain], 0);
+      }
       __syncwarp();
     }
   } else if (warp == 10) {
@@ -403,6 +396,17 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
         }
         lo -= half * 64;
         hi -= half * 64;
+        // Streamed rows of this half behind the sequence's end: clear them (a zero of P or dS times NaN is NaN).
+        const int left = it.y - yt * 128;
+        if (left < 128) {
+          const int r = half * 64 + (row & 63);
+          if (r >= left) {
+            uint8_t* y = smem + L::kY + (st * 2 + (row >> 6)) * L::kTileBytes + r * 128;
+            #pragma unroll
+            for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(y + (c >> 3) * L::kBlock + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
         const bool all = lo <= 0 && hi >= 64;
         const bool warp_all = __all_sync(0xffffffffu, all);
         if (!kKv && it.z == 0) {  // a sequence's first rows: D = sum P dP over the only key tile
