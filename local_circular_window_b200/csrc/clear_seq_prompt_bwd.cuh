@@ -93,7 +93,7 @@ struct PromptBwdLayout {
   static constexpr int kStages = D == 128 ? 2 : 4;        // pairs (Y1, Y2)
   static constexpr int kX = 0;
   static constexpr int kY = kX + 2 * kTileBytes;
-  static constexpr int kStats = kY + kStages * 2 * kTileBytes;  // float2[kStages][128]
+  static constexpr int kStats = kY + kStages * 2 * kTileBytes;  // float[kStages][2][128]: -lse log2 e, -D
   static constexpr int kBars = kStats + kStages * 128 * 8;
   static constexpr int bXFull = 0, bXEmpty = 1;
   static constexpr int bYFull = 2, bYEmpty = bYFull + kStages;
@@ -340,7 +340,7 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
     // ------------------------------------------------------------------ statistics of streamed rows
     regs_dec<kPrRegsLow>();
     if constexpr (kKv) {
-      float2* ring = reinterpret_cast<float2*>(smem + L::kStats);
+      float* ring = reinterpret_cast<float*>(smem + L::kStats);
       int4 it;
       uint32_t slot = 0;
       bool ok = true;
@@ -356,7 +356,10 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
           ok = warp_wait(&bars[L::bStEmpty + s], ((slot / L::kStages) & 1) ^ 1, abort_flag, kDevTimeoutOther, 4, (int)slot);
           if (!ok) break;
           #pragma unroll
-          for (int e = 0; e < 4; ++e) ring[s * 128 + e * 32 + lane] = v[e];
+          for (int e = 0; e < 4; ++e) {
+            ring[s * 256 + e * 32 + lane] = v[e].x;
+            ring[s * 256 + 128 + e * 32 + lane] = v[e].y;
+          }
           mbar_arrive(&bars[L::bStFull + s]);
         }
       }
@@ -370,7 +373,6 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
     const uint32_t s_tm = tmem + lane_base + half * 64;
     const uint32_t d_tm = s_tm + 128;
     const uint64_t sc2 = f32x2_pack(p.scale_log2, p.scale_log2);
-    const float4* stats = reinterpret_cast<const float4*>(smem + L::kStats);
     uint32_t ns = 0, n = 0, slot = 0, nd_phase = 0;
     int4 it;
     while (next_item(&it, 53 + half)) {
@@ -429,42 +431,55 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
           mine.y = -(sums[row] + sums[128 + row]);
           if (half == 0 && valid) p.stats[(long long)it.w * p.n_tok + tok].y = mine.y;
         }
-        #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t s[32], g[32], wp[16], wd[16];
-          tmem_ld32(s_tm + c * 32, s);
-          tmem_ld32(d_tm + c * 32, g);
-          tmem_wait_ld();
+        const float4* nl4 = reinterpret_cast<const float4*>(smem + L::kStats + st * 1024 + half * 256);  // -lse log2 e of the half's columns
+        const float4* nd4 = nl4 + 32;                                                                     // -D
+        const auto tile = [&](auto cut) {
           #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            uint64_t nl, nd;
-            if (kKv) {
-              const float4 v = stats[(st * 128 + half * 64 + c * 32 + 2 * e) >> 1];
-              nl = f32x2_pack(v.x, v.z);
-              nd = f32x2_pack(v.y, v.w);
-            } else {
-              nl = f32x2_pack(mine.x, mine.x);
-              nd = f32x2_pack(mine.y, mine.y);
+          for (int c = 0; c < 2; ++c) {
+            uint32_t s[32], g[32], wp[16], wd[16];
+            tmem_ld32(s_tm + c * 32, s);
+            tmem_ld32(d_tm + c * 32, g);
+            tmem_wait_ld(s);
+            tmem_wait_ld(g);
+            #pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              uint64_t nl[2], nd[2];
+              if (kKv) {
+                const float4 l = nl4[c * 8 + e / 2], m = nd4[c * 8 + e / 2];
+                nl[0] = f32x2_pack(l.x, l.y);
+                nl[1] = f32x2_pack(l.z, l.w);
+                nd[0] = f32x2_pack(m.x, m.y);
+                nd[1] = f32x2_pack(m.z, m.w);
+              } else {
+                nl[0] = nl[1] = f32x2_pack(mine.x, mine.x);
+                nd[0] = nd[1] = f32x2_pack(mine.y, mine.y);
+              }
+              #pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int i0 = 2 * (e + u);
+                const uint64_t x = f32x2_fma(f32x2_pack(__uint_as_float(s[i0]), __uint_as_float(s[i0 + 1])), sc2, nl[u]);
+                float p0 = ex2_approx(f32x2_lo(x)), p1 = ex2_approx(f32x2_hi(x));
+                const uint64_t ds = f32x2_mul(f32x2_pack(p0, p1),
+                                              f32x2_add(f32x2_pack(__uint_as_float(g[i0]), __uint_as_float(g[i0 + 1])), nd[u]));
+                float d0 = f32x2_lo(ds), d1 = f32x2_hi(ds);
+                if constexpr (decltype(cut)::value) {
+                  const int col = c * 32 + i0;
+                  const bool k0 = col >= lo && col < hi, k1 = col + 1 >= lo && col + 1 < hi;
+                  p0 = k0 ? p0 : 0.f;
+                  d0 = k0 ? d0 : 0.f;
+                  p1 = k1 ? p1 : 0.f;
+                  d1 = k1 ? d1 : 0.f;
+                }
+                if (kKv) wp[e + u] = E::pack(p0, p1);
+                wd[e + u] = E::pack(d0, d1);
+              }
             }
-            const uint64_t x = f32x2_fma(f32x2_pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), sc2, nl);
-            float p0 = ex2_approx(f32x2_lo(x)), p1 = ex2_approx(f32x2_hi(x));
-            const uint64_t ds = f32x2_mul(f32x2_pack(p0, p1),
-                                          f32x2_add(f32x2_pack(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1])), nd));
-            float d0 = f32x2_lo(ds), d1 = f32x2_hi(ds);
-            if (!warp_all) {
-              const int col = c * 32 + 2 * e;
-              const bool k0 = col >= lo && col < hi, k1 = col + 1 >= lo && col + 1 < hi;
-              p0 = k0 ? p0 : 0.f;
-              d0 = k0 ? d0 : 0.f;
-              p1 = k1 ? p1 : 0.f;
-              d1 = k1 ? d1 : 0.f;
-            }
-            if (kKv) wp[e] = E::pack(p0, p1);
-            wd[e] = E::pack(d0, d1);
+            if (kKv) tmem_st16(s_tm + c * 16, wp);
+            tmem_st16(d_tm + c * 16, wd);
           }
-          if (kKv) tmem_st16(s_tm + c * 16, wp);
-          tmem_st16(d_tm + c * 16, wd);
-        }
+        };
+        if (warp_all) tile(std::false_type{});
+        else tile(std::true_type{});
         tmem_wait_st();
         warp_arrive_tc(&bars[L::bP + half]);
         if (kKv && lane == 0) mbar_arrive(&bars[L::bStEmpty + st]);
