@@ -4,7 +4,7 @@
 //   dV = P^T dO,  dK = dS^T Q / sqrt(d), both summed over the query heads of the group;  dQ = dS K / sqrt(d).
 //
 // Three launches, deterministic, without atomics:
-//   stats   (-lse log2 e, -D) of every row, one pass over o and dO (bound by memory)
+//   stats   (-lse, -D) of every row, one pass over o and dO (bound by memory)
 //   q       one item per 128-row query tile and query head: Q and dO stay, K and V stream past
 //   kv      one item per 128-key tile and kv head: K and V stay, the group's Q and dO stream past
 // S and dP are computed in both, seven products in place of five: the price of writing every gradient
@@ -20,7 +20,16 @@
 // P and dS, rounded to the element type over the scores (two values a column); the accumulating
 // products read them from TMEM. One half's products run while the other half's warpgroup computes.
 //   warps 0-3 / 4-7  half 0 / 1: a thread owns one row of X and 64 columns
-//   warp 8 TMA, warp 9 products, warp 10 items, warp 11 the streamed rows' statistics (kv)
+//   warp 8 TMA, warp 9 products (one thread), warp 10 items, warp 11 the streamed rows' statistics (kv)
+// The streamed tiles go through a ring of halves (64 rows of Y1 and of Y2), each released by its own
+// accumulating products: whole pairs left the loads half a step's time only.
+//
+// Statistics of streamed rows (kv) would be needed per column of S^T, by every thread for every column: read from
+// shared memory, against the products' operands, they took 800 of 2000 cycles a half. They ride along in the
+// products instead: one more step of 16 along the reduced axis, X = constants, Y = -lse sqrt(d) and -D as
+// three parts each of 16-bit type, whose products with the constants add up to the fp32 value (24 bits
+// and more). P = 2^(S' log2 e / sqrt(d)) and dS = P dP' then need no other input.
+//
 // Rounding P and dS costs half a step of each, of random sign; sums, statistics and accumulators are fp32.
 //
 // D from the given o carries o's rounding, which dS = P (dP - D) shares along the whole row: against the
@@ -41,7 +50,7 @@ namespace clear {
 
 struct SeqBwdParams {
   SeqView out1, out2;    // kv: dv, dk; q: -, dq
-  float2* stats;         // [q_heads, n_tok]: (-lse log2 e, -D)
+  float2* stats;         // [q_heads, n_tok]: (-lse, -D)
   const int* seq_start;
   int n_seq, n_tok, q_heads, kv_heads, group;
   float scale, scale_log2;
@@ -82,35 +91,64 @@ __global__ void __launch_bounds__(kStatsThreads) clear_seq_bwd_stats_kernel(cons
   if (in && lane == 0) {
     const float l = __ldg(p.lse + (long long)h * p.n_tok + t);
     // A row without a finite score (lse -inf) has P = 0: 2^(-inf) instead of 2^(-inf + inf).
-    p.stats[(long long)h * p.n_tok + t] = make_float2(l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f, -sum);
+    p.stats[(long long)h * p.n_tok + t] = make_float2(l == -INFINITY ? -INFINITY : -l, -sum);
   }
 }
 
 template <int D>
 struct PromptBwdLayout {
   static constexpr int kTileBytes = 128 * D * 2;
-  static constexpr int kBlock = 128 * 128;
-  static constexpr int kStages = D == 128 ? 2 : 4;        // pairs (Y1, Y2)
-  static constexpr int kX = 0;
+  static constexpr int kBlock = 128 * 128;                // X: 128 rows x 64 elements
+  static constexpr int kHalfTile = 64 * D * 2;
+  static constexpr int kYBlock = 64 * 128;                // Y: 64 rows x 64 elements
+  static constexpr int kStages = D == 128 ? 4 : 8;        // halves of (Y1, Y2)
+  static constexpr int kStageBytes = 2 * kHalfTile;
+  // Statistics as operands, in 8-row x 16-byte blocks without swizzle: per stage 64 rows of 8 values; then 128 rows
+  // of constants for S, 128 for dP and 128 rows of zeros (the second half of each 16-step).
+  static constexpr int kAug = 0;
+  static constexpr int kOnes = kAug + kStages * 1024;
+  static constexpr int kZeros = kOnes + 4096;
+  static constexpr int kX = kOnes + 6144;
   static constexpr int kY = kX + 2 * kTileBytes;
-  static constexpr int kStats = kY + kStages * 2 * kTileBytes;  // float[kStages][2][128]: -lse log2 e, -D
-  static constexpr int kBars = kStats + kStages * 128 * 8;
+  static constexpr int kBars = kY + kStages * kStageBytes;
+  static_assert(kX % 1024 == 0 && kBars % 16 == 0, "alignment");
   static constexpr int bXFull = 0, bXEmpty = 1;
   static constexpr int bYFull = 2, bYEmpty = bYFull + kStages;
-  static constexpr int bStFull = bYEmpty + kStages, bStEmpty = bStFull + kStages;
-  static constexpr int bS = bStEmpty + kStages;           // + half: S and dP written
+  static constexpr int bS = bYEmpty + kStages;            // + half: S and dP written
   static constexpr int bP = bS + 2;                       // + half: P and dS written
   static constexpr int bAcc = bP + 2;                     // the item's last accumulating product done
   static constexpr int bAccFree = bAcc + 1;               // the accumulators have been read
   static constexpr int bItemFull = bAccFree + 1, bItemEmpty = bItemFull + kPrItems;
   static constexpr int bDrain = bItemEmpty + kPrItems;
-  static constexpr int bD = bDrain + 1;                   // both halves' sums of a first tile (in the statistics' place)
+  static constexpr int bD = bDrain + 1;                   // both halves' sums of a first tile (q: in the statistics' place)
   static constexpr int kNumBars = bD + 1;
   static constexpr int kItems = (kBars + kNumBars * 8 + 15) & ~15;
   static constexpr int kMisc = kItems + kPrItems * 16;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static_assert(kAlloc <= 232448, "shared memory");
 };
+
+// A matrix descriptor without swizzle: 8-row x 16-byte blocks, k_step bytes apart along the reduced axis and 128 along the rows.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t k_step) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((k_step >> 4) & 0x3FFFu) << 16) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1u << 46);
+}
+
+// v as three 16-bit parts: v = c0 a + c1 b + c2 c with the constants below. bf16 has fp32's range: the constants
+// are 1, each part takes 8 bits. fp16 takes 11 bits each; its constants (2^7, 2^-3, 2^-13) reach from 8e6 down to steps of
+// 2^-37. Larger values are cut to the limit (P is 0 then, or the gradient out of fp16's range).
+template <typename E>
+__device__ __forceinline__ void split3(float v, uint32_t* ab, uint32_t* c) {
+  constexpr bool kB = std::is_same<E, Bf16>::value;
+  constexpr float kLimit = kB ? 1e30f : 8e6f;
+  constexpr float c0 = kB ? 1.f : 128.f, c1 = kB ? 1.f : 0.125f, c2 = kB ? 1.f : 1.f / 8192.f;
+  v = v > kLimit ? kLimit : v < -kLimit ? -kLimit : v;
+  const uint32_t w0 = E::pack(v / c0, 0.f);
+  v = fmaf(-c0, E::lo(w0), v);
+  const uint32_t w1 = E::pack(v / c1, 0.f);
+  v = fmaf(-c1, E::lo(w1), v);
+  *ab = (w0 & 0xffffu) | (w1 << 16);
+  *c = E::pack(v / c2, 0.f) & 0xffffu;
+}
 
 // An item as the ring carries it: {the sequence's first token, its length (0: end of the list), X tile, head}.
 template <typename E, int D, bool kKv>
@@ -132,10 +170,8 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
     mbar_init(&bars[L::bXFull], 1);
     mbar_init(&bars[L::bXEmpty], 1);
     for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(&bars[L::bYFull + s], 1);
+      mbar_init(&bars[L::bYFull + s], kKv ? 2 : 1);  // the copies, and the statistics' warp
       mbar_init(&bars[L::bYEmpty + s], 1);
-      mbar_init(&bars[L::bStFull + s], 32);
-      mbar_init(&bars[L::bStEmpty + s], 8);
     }
     for (int h = 0; h < 2; ++h) {
       mbar_init(&bars[L::bS + h], 1);
@@ -155,6 +191,16 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
   if (warp == 9) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
+  }
+  if (kKv) {  // the constants that the statistics' parts are multiplied with: columns 0-2 for S, 3-5 for dP
+    const int which = threadIdx.x >> 7, r = threadIdx.x & 127;
+    constexpr bool kB = std::is_same<E, Bf16>::value;
+    const uint32_t ab = E::pack(kB ? 1.f : 128.f, kB ? 1.f : 0.125f), c = E::pack(kB ? 1.f : 1.f / 8192.f, 0.f) & 0xffffu;
+    const uint4 w = which == 0   ? make_uint4(ab, c, 0, 0)
+                    : which == 1 ? make_uint4(0, ab << 16, (ab >> 16) | (c << 16), 0)
+                                 : make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(smem + L::kOnes + which * 2048 + r * 16) = w;
+    fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
@@ -192,16 +238,20 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
           load_seq_tile<D>(smem + L::kX + L::kTileBytes, &tm_x2, &bars[L::bXFull], it.x + it.z * 128, it.w);
           ++x_loads;
         }
-        for (int i = 0; i < steps && ok; ++i) {
+        for (int i = 0; i < 2 * steps && ok; ++i) {  // halves
           const uint32_t s = slot % L::kStages;
           ok = seq_wait(&bars[L::bYEmpty + s], ((slot / L::kStages) & 1) ^ 1, abort_flag, kDevTimeoutTmaEmpty, 2, (int)n, i);
           if (!ok) break;
-          const int tile = kKv ? it.z + i % per : i;
-          const int head = kKv ? it.w * p.group + i / per : it.w / p.group;
-          uint8_t* dst = smem + L::kY + s * 2 * L::kTileBytes;
-          mbar_arrive_expect_tx(&bars[L::bYFull + s], 2 * L::kTileBytes);
-          load_seq_tile<D>(dst, &tm_y1, &bars[L::bYFull + s], it.x + tile * 128, head);
-          load_seq_tile<D>(dst + L::kTileBytes, &tm_y2, &bars[L::bYFull + s], it.x + tile * 128, head);
+          const int tile = kKv ? it.z + (i >> 1) % per : i >> 1;
+          const int head = kKv ? it.w * p.group + (i >> 1) / per : it.w / p.group;
+          const int tok = it.x + tile * 128 + (i & 1) * 64;
+          uint8_t* dst = smem + L::kY + s * L::kStageBytes;
+          mbar_arrive_expect_tx(&bars[L::bYFull + s], L::kStageBytes);
+          #pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            tma_load_3d(dst + c * L::kYBlock, &tm_y1, &bars[L::bYFull + s], c * 64, tok, head);
+            tma_load_3d(dst + L::kHalfTile + c * L::kYBlock, &tm_y2, &bars[L::bYFull + s], c * 64, tok, head);
+          }
           ++slot;
         }
       }
@@ -221,7 +271,7 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
     constexpr uint32_t idesc_a = idesc_seq<E>(128, D, 0, 1);
     const uint64_t xdesc = smem_desc_sw128(smem_u32(smem + L::kX), 16, 1024);
     const uint64_t ykdesc = smem_desc_sw128(smem_u32(smem + L::kY), 16, 1024);         // as K-major B operand
-    const uint64_t ymdesc = smem_desc_sw128(smem_u32(smem + L::kY), L::kBlock, 1024);  // as MN-major B operand
+    const uint64_t ymdesc = smem_desc_sw128(smem_u32(smem + L::kY), L::kYBlock, 1024);  // as MN-major B operand
     int4 it;
     uint32_t n = 0, np = 0;         // items; streamed pairs
     uint32_t stage = 0, phase = 0;  // of the next pair in the ring
@@ -229,16 +279,19 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
     while (ok && next_item(&it, 51)) {
       if (elect_one()) {
         const int steps = steps_of(it);
-        // S_h and dP_h of the streamed pair in stage s
+        // S_h and dP_h of the streamed half in stage s
         const auto scores = [&](int h, uint32_t s) {
-          const uint64_t yd = ykdesc + (uint64_t)((s * 2 * L::kTileBytes + h * 8192) >> 4);
+          const uint64_t yd = ykdesc + (uint64_t)((s * L::kStageBytes) >> 4);
           #pragma unroll
           for (int x = 0; x < 2; ++x) {
             #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = ((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4;
-              umma_ss(tmem + x * 128 + h * 64, xdesc + ((x * L::kTileBytes) >> 4) + off, yd + ((x * L::kTileBytes) >> 4) + off,
-                      idesc_s, kk > 0);
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_ss(tmem + x * 128 + h * 64, xdesc + ((x * L::kTileBytes + (kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4),
+                      yd + ((x * L::kHalfTile + (kk >> 2) * L::kYBlock + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+            if (kKv) {
+              const uint32_t aug = L::kAug + s * 1024, ones = L::kOnes + x * 2048;
+              umma_ss(tmem + x * 128 + h * 64, smem_desc_plain(smem_u32(smem + ones), L::kZeros - ones),
+                      smem_desc_plain(smem_u32(smem + aug), L::kZeros - aug), idesc_s, 1);
             }
           }
           umma_commit(&bars[L::bS + h]);
@@ -247,44 +300,48 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
           ok = ok && seq_wait(&bars[L::bP + h], np & 1, abort_flag, kDevTimeoutMma, 12 + h, (int)n, (int)np);
           if (!ok) return;
           tc_fence_after();
-          const uint64_t yd = ymdesc + (uint64_t)((s * 2 * L::kTileBytes + h * 8192) >> 4);
+          const uint64_t yd = ymdesc + (uint64_t)((s * L::kStageBytes) >> 4);
           if (kKv) {
             #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_ts(tmem + 256, tmem + h * 64 + kk * 8, yd + ((L::kTileBytes + kk * 2048) >> 4), idesc_a, (!first || kk > 0) ? 1u : 0u);
+              umma_ts(tmem + 256, tmem + h * 64 + kk * 8, yd + ((L::kHalfTile + kk * 2048) >> 4), idesc_a, (!first || kk > 0) ? 1u : 0u);
           }
           #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             umma_ts(tmem + 256 + D, tmem + 128 + h * 64 + kk * 8, yd + ((kk * 2048) >> 4), idesc_a, (!first || kk > 0) ? 1u : 0u);
+          umma_commit(&bars[L::bYEmpty + s]);
         };
-        const auto ready = [&](uint32_t s, uint32_t ph, int i) {
-          ok = ok && seq_wait(&bars[L::bYFull + s], ph, abort_flag, kDevTimeoutMma, 11, (int)n, i);
+        // The next half in the ring: waits for it and moves on.
+        const auto next_half = [&](int i) {
+          const uint32_t s = stage;
+          ok = ok && seq_wait(&bars[L::bYFull + s], phase, abort_flag, kDevTimeoutMma, 11, (int)n, i);
+          if (++stage == L::kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+          return s;
         };
         ok = seq_wait(&bars[L::bXFull], n & 1, abort_flag, kDevTimeoutMma, 10, (int)n);
-        ready(stage, phase, 0);
+        uint32_t s0 = next_half(0);
+        if (ok) scores(0, s0);
+        uint32_t s1 = next_half(0);
         if (ok) {
-          scores(0, stage);
-          scores(1, stage);
+          scores(1, s1);
           if (steps == 1) umma_commit(&bars[L::bXEmpty]);
           // The accumulators are free once the previous item's have been written out.
           ok = seq_wait(&bars[L::bAccFree], (n & 1) ^ 1, abort_flag, kDevTimeoutMma, 14, (int)n);
         }
         for (int i = 0; i < steps && ok; ++i) {
-          const uint32_t s = stage;
-          if (++stage == L::kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
           const bool more = i + 1 < steps;
-          if (more) ready(stage, phase, i + 1);
-          accumulate(0, s, i == 0);
+          accumulate(0, s0, i == 0);
+          if (more) s0 = next_half(i + 1);
           if (!ok) break;
-          if (more) scores(0, stage);
-          accumulate(1, s, false);
+          if (more) scores(0, s0);
+          accumulate(1, s1, false);
+          if (more) s1 = next_half(i + 1);
           if (!ok) break;
           ++np;
-          umma_commit(&bars[L::bYEmpty + s]);
-          if (more) scores(1, stage);
+          if (more) scores(1, s1);
           if (i + 2 == steps) umma_commit(&bars[L::bXEmpty]);
         }
         if (ok) umma_commit(&bars[L::bAcc]);
@@ -340,27 +397,32 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
     // ------------------------------------------------------------------ statistics of streamed rows
     regs_dec<kPrRegsLow>();
     if constexpr (kKv) {
-      float* ring = reinterpret_cast<float*>(smem + L::kStats);
+      const float root = 1.f / p.scale;  // sqrt(d)
       int4 it;
       uint32_t slot = 0;
       bool ok = true;
       while (ok && next_item(&it, 52)) {
         const int steps = steps_of(it), per = n_tiles(it) - it.z;
-        for (int i = 0; i < steps; ++i, ++slot) {
-          const int t0 = (it.z + i % per) * 128;
-          const float2* src = p.stats + (long long)(it.w * p.group + i / per) * p.n_tok + it.x + t0;
-          float2 v[4];
+        for (int i = 0; i < 2 * steps; ++i, ++slot) {
+          const int t0 = (it.z + (i >> 1) % per) * 128 + (i & 1) * 64;
+          const float2* src = p.stats + (long long)(it.w * p.group + (i >> 1) / per) * p.n_tok + it.x + t0;
+          float2 v[2];
           #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = t0 + e * 32 + lane < it.y ? src[e * 32 + lane] : make_float2(0.f, 0.f);
+          for (int e = 0; e < 2; ++e) v[e] = t0 + e * 32 + lane < it.y ? src[e * 32 + lane] : make_float2(0.f, 0.f);
           const uint32_t s = slot % L::kStages;
-          ok = warp_wait(&bars[L::bStEmpty + s], ((slot / L::kStages) & 1) ^ 1, abort_flag, kDevTimeoutOther, 4, (int)slot);
+          ok = warp_wait(&bars[L::bYEmpty + s], ((slot / L::kStages) & 1) ^ 1, abort_flag, kDevTimeoutOther, 4, (int)slot);
           if (!ok) break;
           #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            ring[s * 256 + e * 32 + lane] = v[e].x;
-            ring[s * 256 + 128 + e * 32 + lane] = v[e].y;
+          for (int e = 0; e < 2; ++e) {
+            uint32_t l01, l2, d01, d2;
+            split3<E>(v[e].x * root, &l01, &l2);
+            split3<E>(v[e].y, &d01, &d2);
+            *reinterpret_cast<uint4*>(smem + L::kAug + s * 1024 + (e * 32 + lane) * 16) =
+                make_uint4(l01, l2 | (d01 << 16), (d01 >> 16) | (d2 << 16), 0);
           }
-          mbar_arrive(&bars[L::bStFull + s]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[L::bYFull + s]);
         }
       }
     }
@@ -380,11 +442,13 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
       const bool valid = it.z * 128 + row < it.y;
       const long long tok = (long long)it.x + it.z * 128 + row;
       float2 mine = make_float2(0.f, 0.f);
-      if (!kKv && valid) mine = p.stats[(long long)it.w * p.n_tok + tok];
+      if (!kKv && valid) {
+        mine = p.stats[(long long)it.w * p.n_tok + tok];
+        mine.x *= 1.4426950408889634f;
+      }
       for (int i = 0; i < steps; ++i, ++slot) {
         const int yt = kKv ? it.z + i % per : i;
-        const uint32_t st = slot % L::kStages;
-        if (kKv && !warp_wait(&bars[L::bStFull + st], (slot / L::kStages) & 1, abort_flag, kDevTimeoutSoftmax, 22 + half, (int)slot)) goto done;
+        const uint32_t st = (2 * slot + half) % L::kStages;
         if (!warp_wait(&bars[L::bS + half], ns & 1, abort_flag, kDevTimeoutSoftmax, 20 + half, (int)ns, i)) goto done;
         ++ns;
         tc_fence_after();
@@ -403,9 +467,9 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
         if (left < 128) {
           const int r = half * 64 + (row & 63);
           if (r >= left) {
-            uint8_t* y = smem + L::kY + (st * 2 + (row >> 6)) * L::kTileBytes + r * 128;
+            uint8_t* y = smem + L::kY + st * L::kStageBytes + (row >> 6) * L::kHalfTile + (row & 63) * 128;
             #pragma unroll
-            for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(y + (c >> 3) * L::kBlock + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(y + (c >> 3) * L::kYBlock + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
@@ -423,7 +487,7 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
             for (int e = 0; e < 32; ++e)
               if (c * 32 + e < hi) sum = fmaf(ex2_approx(fmaf(__uint_as_float(s[e]), p.scale_log2, mine.x)), __uint_as_float(g[e]), sum);
           }
-          float* sums = reinterpret_cast<float*>(smem + L::kStats);
+          float* sums = reinterpret_cast<float*>(smem + L::kAug);
           sums[half * 128 + row] = sum;
           mbar_arrive(&bars[L::bD]);
           if (!warp_wait(&bars[L::bD], nd_phase & 1, abort_flag, kDevTimeoutSoftmax, 26 + half, (int)nd_phase)) goto done;
@@ -431,8 +495,6 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
           mine.y = -(sums[row] + sums[128 + row]);
           if (half == 0 && valid) p.stats[(long long)it.w * p.n_tok + tok].y = mine.y;
         }
-        const float4* nl4 = reinterpret_cast<const float4*>(smem + L::kStats + st * 1024 + half * 256);  // -lse log2 e of the half's columns
-        const float4* nd4 = nl4 + 32;                                                                     // -D
         const auto tile = [&](auto cut) {
           #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -442,37 +504,23 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
             tmem_wait_ld(s);
             tmem_wait_ld(g);
             #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              uint64_t nl[2], nd[2];
-              if (kKv) {
-                const float4 l = nl4[c * 8 + e / 2], m = nd4[c * 8 + e / 2];
-                nl[0] = f32x2_pack(l.x, l.y);
-                nl[1] = f32x2_pack(l.z, l.w);
-                nd[0] = f32x2_pack(m.x, m.y);
-                nd[1] = f32x2_pack(m.z, m.w);
-              } else {
-                nl[0] = nl[1] = f32x2_pack(mine.x, mine.x);
-                nd[0] = nd[1] = f32x2_pack(mine.y, mine.y);
+            for (int e = 0; e < 16; ++e) {
+              const uint64_t s2 = f32x2_pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+              const uint64_t g2 = f32x2_pack(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1]));
+              const uint64_t x = kKv ? f32x2_mul(s2, sc2) : f32x2_fma(s2, sc2, f32x2_pack(mine.x, mine.x));
+              float p0 = ex2_approx(f32x2_lo(x)), p1 = ex2_approx(f32x2_hi(x));
+              const uint64_t ds = f32x2_mul(f32x2_pack(p0, p1), kKv ? g2 : f32x2_add(g2, f32x2_pack(mine.y, mine.y)));
+              float d0 = f32x2_lo(ds), d1 = f32x2_hi(ds);
+              if constexpr (decltype(cut)::value) {
+                const int col = c * 32 + 2 * e;
+                const bool k0 = col >= lo && col < hi, k1 = col + 1 >= lo && col + 1 < hi;
+                p0 = k0 ? p0 : 0.f;
+                d0 = k0 ? d0 : 0.f;
+                p1 = k1 ? p1 : 0.f;
+                d1 = k1 ? d1 : 0.f;
               }
-              #pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int i0 = 2 * (e + u);
-                const uint64_t x = f32x2_fma(f32x2_pack(__uint_as_float(s[i0]), __uint_as_float(s[i0 + 1])), sc2, nl[u]);
-                float p0 = ex2_approx(f32x2_lo(x)), p1 = ex2_approx(f32x2_hi(x));
-                const uint64_t ds = f32x2_mul(f32x2_pack(p0, p1),
-                                              f32x2_add(f32x2_pack(__uint_as_float(g[i0]), __uint_as_float(g[i0 + 1])), nd[u]));
-                float d0 = f32x2_lo(ds), d1 = f32x2_hi(ds);
-                if constexpr (decltype(cut)::value) {
-                  const int col = c * 32 + i0;
-                  const bool k0 = col >= lo && col < hi, k1 = col + 1 >= lo && col + 1 < hi;
-                  p0 = k0 ? p0 : 0.f;
-                  d0 = k0 ? d0 : 0.f;
-                  p1 = k1 ? p1 : 0.f;
-                  d1 = k1 ? d1 : 0.f;
-                }
-                if (kKv) wp[e + u] = E::pack(p0, p1);
-                wd[e + u] = E::pack(d0, d1);
-              }
+              if (kKv) wp[e] = E::pack(p0, p1);
+              wd[e] = E::pack(d0, d1);
             }
             if (kKv) tmem_st16(s_tm + c * 16, wp);
             tmem_st16(d_tm + c * 16, wd);
@@ -482,7 +530,6 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
         else tile(std::true_type{});
         tmem_wait_st();
         warp_arrive_tc(&bars[L::bP + half]);
-        if (kKv && lane == 0) mbar_arrive(&bars[L::bStEmpty + st]);
       }
       // ---- epilogue: kv: this half writes dv (0) or dk (1); q: its half of dq's columns
       if (!warp_wait(&bars[L::bAcc], n & 1, abort_flag, kDevTimeoutSoftmax, 24 + half, (int)n)) goto done;
