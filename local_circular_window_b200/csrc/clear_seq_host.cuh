@@ -194,7 +194,8 @@ template <typename E, int D>
 clear_status_t launch_prompt_bwd(const clear_seq_params_t* sp, const SeqView& q, const SeqView& k, const SeqView& v, const SeqView& g,
                                  const SeqView& dq, const SeqView& dk, const SeqView& dv, const SeqStatsParams& st, SeqBwdParams p,
                                  int num_sms, cudaStream_t stream) {
-  using L = PromptBwdLayout<D>;
+  using LK = PromptBwdLayout<D, true>;
+  using LQ = PromptBwdLayout<D, false>;
   // Tiles that stay come 128 rows at a time, tiles that stream 64.
   CUtensorMap mq, mk, mv, mg, sq, sk, sv, sg;
   if (!make_seq_map(&mq, q, sp->q_heads, sp->n_tok, D, sp->dtype) || !make_seq_map(&mk, k, sp->kv_heads, sp->n_tok, D, sp->dtype) ||
@@ -203,18 +204,18 @@ clear_status_t launch_prompt_bwd(const clear_seq_params_t* sp, const SeqView& q,
       !make_seq_map(&sv, v, sp->kv_heads, sp->n_tok, D, sp->dtype, 64) || !make_seq_map(&sg, g, sp->q_heads, sp->n_tok, D, sp->dtype, 64))
     return CLEAR_ERR_CUDA;
   static std::atomic<unsigned long long> done[2];
-  if (!allow_smem(reinterpret_cast<const void*>(clear_seq_prompt_bwd_kernel<E, D, true>), L::kAlloc, &done[0]) ||
-      !allow_smem(reinterpret_cast<const void*>(clear_seq_prompt_bwd_kernel<E, D, false>), L::kAlloc, &done[1]))
+  if (!allow_smem(reinterpret_cast<const void*>(clear_seq_prompt_bwd_kernel<E, D, true>), LK::kAlloc, &done[0]) ||
+      !allow_smem(reinterpret_cast<const void*>(clear_seq_prompt_bwd_kernel<E, D, false>), LQ::kAlloc, &done[1]))
     return CLEAR_ERR_CUDA;
   const long long lanes = (long long)sp->n_tok * sp->q_heads * (D / 8);
   clear_seq_bwd_stats_kernel<E, D><<<(unsigned)((lanes + kStatsThreads - 1) / kStatsThreads), kStatsThreads, 0, stream>>>(st);
   if (cudaGetLastError() != cudaSuccess) return CLEAR_ERR_CUDA;
   p.out2 = dq;  // first: it settles the first rows' statistics for the other
-  clear_seq_prompt_bwd_kernel<E, D, false><<<prompt_blocks(sp, 128, sp->q_heads, num_sms), kPrThreads, L::kAlloc, stream>>>(mq, mg, sk, sv, p);
+  clear_seq_prompt_bwd_kernel<E, D, false><<<prompt_blocks(sp, 128, sp->q_heads, num_sms), kPrThreads, LQ::kAlloc, stream>>>(mq, mg, sk, sv, p);
   if (cudaGetLastError() != cudaSuccess) return CLEAR_ERR_CUDA;
   p.out1 = dv;
   p.out2 = dk;
-  clear_seq_prompt_bwd_kernel<E, D, true><<<prompt_blocks(sp, 128, sp->kv_heads, num_sms), kPrThreads, L::kAlloc, stream>>>(mk, mv, sq, sg, p);
+  clear_seq_prompt_bwd_kernel<E, D, true><<<prompt_blocks(sp, 128, sp->kv_heads, num_sms), kPrThreads, LK::kAlloc, stream>>>(mk, mv, sq, sg, p);
   return cudaGetLastError() == cudaSuccess ? CLEAR_OK : CLEAR_ERR_CUDA;
 }
 

@@ -16,7 +16,7 @@
 //            X1  X2   Y1  Y2    scores (rows = X)   acc1 +=     acc2 +=
 //   kv       K   V    Q   dO    S^T, dP^T           P^T Y2      dS^T Y1
 //   q        Q   dO   K   V     S,   dP                         dS Y1
-// Per half h: S_h = X1 Y1_h^T and dP_h = X2 Y2_h^T into TMEM; a warpgroup of its own turns them into
+// Per half: S = X1 Y1^T and dP = X2 Y2^T into one of two or three TMEM buffers; a warpgroup turns them into
 // P and dS, rounded to the element type over the scores (two values a column); the accumulating
 // products read them from TMEM. One half's products run while the other half's warpgroup computes.
 //   warps 0-3 / 4-7  half 0 / 1: a thread owns one row of X and 64 columns
@@ -95,8 +95,14 @@ __global__ void __launch_bounds__(kStatsThreads) clear_seq_bwd_stats_kernel(cons
   }
 }
 
-template <int D>
+template <int D, bool kKv>
 struct PromptBwdLayout {
+  // TMEM: half buffers of S (64 columns) and dP (64), then the accumulators. At d = 64 the products are short and a third
+  // buffer has the next half's scores there before its warpgroup has finished the last one's (dQ 45 to 39 us on 4096
+  // packed tokens of 16 heads); at d = 128 kv has no room for one, and q ran no faster with it.
+  static constexpr int kBufs = D == 128 ? 2 : 3;
+  static constexpr int kAcc1 = kBufs * 128, kAcc2 = kAcc1 + (kKv ? D : 0);
+  static_assert(kAcc2 + D <= 512, "tensor memory");
   static constexpr int kTileBytes = 128 * D * 2;
   static constexpr int kBlock = 128 * 128;                // X: 128 rows x 64 elements
   static constexpr int kHalfTile = 64 * D * 2;
@@ -114,9 +120,9 @@ struct PromptBwdLayout {
   static_assert(kX % 1024 == 0 && kBars % 16 == 0, "alignment");
   static constexpr int bXFull = 0, bXEmpty = 1;
   static constexpr int bYFull = 2, bYEmpty = bYFull + kStages;
-  static constexpr int bS = bYEmpty + kStages;            // + half: S and dP written
-  static constexpr int bP = bS + 2;                       // + half: P and dS written
-  static constexpr int bAcc = bP + 2;                     // the item's last accumulating product done
+  static constexpr int bS = bYEmpty + kStages;            // + buffer: S and dP written
+  static constexpr int bP = bS + kBufs;                   // + buffer: P and dS written
+  static constexpr int bAcc = bP + kBufs;                     // the item's last accumulating product done
   static constexpr int bAccFree = bAcc + 1;               // the accumulators have been read
   static constexpr int bItemFull = bAccFree + 1, bItemEmpty = bItemFull + kPrItems;
   static constexpr int bDrain = bItemEmpty + kPrItems;
@@ -156,7 +162,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_x2,
                             const __grid_constant__ CUtensorMap tm_y1, const __grid_constant__ CUtensorMap tm_y2,
                             const __grid_constant__ SeqBwdParams p) {
-  using L = PromptBwdLayout<D>;
+  using L = PromptBwdLayout<D, kKv>;
   using T = typename E::type;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -173,9 +179,9 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
       mbar_init(&bars[L::bYFull + s], kKv ? 2 : 1);  // the copies, and the statistics' warp
       mbar_init(&bars[L::bYEmpty + s], 1);
     }
-    for (int h = 0; h < 2; ++h) {
-      mbar_init(&bars[L::bS + h], 1);
-      mbar_init(&bars[L::bP + h], 4);
+    for (int i = 0; i < L::kBufs; ++i) {
+      mbar_init(&bars[L::bS + i], 1);
+      mbar_init(&bars[L::bP + i], 4);
     }
     mbar_init(&bars[L::bAcc], 1);
     mbar_init(&bars[L::bAccFree], 8);
@@ -273,42 +279,44 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
     const uint64_t ykdesc = smem_desc_sw128(smem_u32(smem + L::kY), 16, 1024);         // as K-major B operand
     const uint64_t ymdesc = smem_desc_sw128(smem_u32(smem + L::kY), L::kYBlock, 1024);  // as MN-major B operand
     int4 it;
-    uint32_t n = 0, np = 0;         // items; streamed pairs
+    uint32_t n = 0;                 // items
+    uint32_t np = 0;                // bit b: the phase of buffer b's next P and dS
     uint32_t stage = 0, phase = 0;  // of the next pair in the ring
     bool ok = true;
     while (ok && next_item(&it, 51)) {
       if (elect_one()) {
         const int steps = steps_of(it);
-        // S_h and dP_h of the streamed half in stage s
-        const auto scores = [&](int h, uint32_t s) {
+        // S and dP of the streamed half in stage s, into buffer b
+        const auto scores = [&](uint32_t b, uint32_t s) {
           const uint64_t yd = ykdesc + (uint64_t)((s * L::kStageBytes) >> 4);
           #pragma unroll
           for (int x = 0; x < 2; ++x) {
             #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              umma_ss(tmem + x * 128 + h * 64, xdesc + ((x * L::kTileBytes + (kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4),
+              umma_ss(tmem + b * 128 + x * 64, xdesc + ((x * L::kTileBytes + (kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4),
                       yd + ((x * L::kHalfTile + (kk >> 2) * L::kYBlock + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
             if (kKv) {
               const uint32_t aug = L::kAug + s * 1024, ones = L::kOnes + x * 2048;
-              umma_ss(tmem + x * 128 + h * 64, smem_desc_plain(smem_u32(smem + ones), L::kZeros - ones),
+              umma_ss(tmem + b * 128 + x * 64, smem_desc_plain(smem_u32(smem + ones), L::kZeros - ones),
                       smem_desc_plain(smem_u32(smem + aug), L::kZeros - aug), idesc_s, 1);
             }
           }
-          umma_commit(&bars[L::bS + h]);
+          umma_commit(&bars[L::bS + b]);
         };
-        const auto accumulate = [&](int h, uint32_t s, bool first) {
-          ok = ok && seq_wait(&bars[L::bP + h], np & 1, abort_flag, kDevTimeoutMma, 12 + h, (int)n, (int)np);
+        const auto accumulate = [&](uint32_t buf, uint32_t s, bool first) {
+          ok = ok && seq_wait(&bars[L::bP + buf], (np >> buf) & 1, abort_flag, kDevTimeoutMma, 12, (int)n, (int)s);
           if (!ok) return;
+          np ^= 1u << buf;
           tc_fence_after();
           const uint64_t yd = ymdesc + (uint64_t)((s * L::kStageBytes) >> 4);
           if (kKv) {
             #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_ts(tmem + 256, tmem + h * 64 + kk * 8, yd + ((L::kHalfTile + kk * 2048) >> 4), idesc_a, (!first || kk > 0) ? 1u : 0u);
+              umma_ts(tmem + L::kAcc1, tmem + buf * 128 + kk * 8, yd + ((L::kHalfTile + kk * 2048) >> 4), idesc_a, (!first || kk > 0) ? 1u : 0u);
           }
           #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_ts(tmem + 256 + D, tmem + 128 + h * 64 + kk * 8, yd + ((kk * 2048) >> 4), idesc_a, (!first || kk > 0) ? 1u : 0u);
+            umma_ts(tmem + L::kAcc2, tmem + buf * 128 + 64 + kk * 8, yd + ((kk * 2048) >> 4), idesc_a, (!first || kk > 0) ? 1u : 0u);
           umma_commit(&bars[L::bYEmpty + s]);
         };
         // The next half in the ring: waits for it and moves on.
@@ -322,27 +330,30 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
           return s;
         };
         ok = seq_wait(&bars[L::bXFull], n & 1, abort_flag, kDevTimeoutMma, 10, (int)n);
-        uint32_t s0 = next_half(0);
-        if (ok) scores(0, s0);
-        uint32_t s1 = next_half(0);
-        if (ok) {
-          scores(1, s1);
-          if (steps == 1) umma_commit(&bars[L::bXEmpty]);
-          // The accumulators are free once the previous item's have been written out.
-          ok = seq_wait(&bars[L::bAccFree], (n & 1) ^ 1, abort_flag, kDevTimeoutMma, 14, (int)n);
+        const int halves = 2 * steps;
+        int ahead = 0;           // halves whose scores have been issued
+        uint32_t st[L::kBufs];   // the stage of each buffer's half
+        const auto issue_scores = [&](uint32_t b) {
+          const uint32_t x = next_half(ahead);
+          if (ok) scores(b, x);
+          if (ok && ++ahead == halves) umma_commit(&bars[L::bXEmpty]);
+          return x;
+        };
+        #pragma unroll
+        for (int u = 0; u < L::kBufs; ++u) {
+          st[u] = 0;
+          if (u < halves && ok) st[u] = issue_scores(u);
         }
-        for (int i = 0; i < steps && ok; ++i) {
-          const bool more = i + 1 < steps;
-          accumulate(0, s0, i == 0);
-          if (more) s0 = next_half(i + 1);
-          if (!ok) break;
-          if (more) scores(0, s0);
-          accumulate(1, s1, false);
-          if (more) s1 = next_half(i + 1);
-          if (!ok) break;
-          ++np;
-          if (more) scores(1, s1);
-          if (i + 2 == steps) umma_commit(&bars[L::bXEmpty]);
+        // The accumulators are free once the previous item's have been written out.
+        ok = ok && seq_wait(&bars[L::bAccFree], (n & 1) ^ 1, abort_flag, kDevTimeoutMma, 14, (int)n);
+        for (int i = 0; i < halves && ok; i += L::kBufs) {
+          #pragma unroll
+          for (int u = 0; u < L::kBufs; ++u) {
+            if (i + u < halves && ok) {
+              accumulate(u, st[u], i + u == 0);
+              if (ok && ahead < halves) st[u] = issue_scores(u);
+            }
+          }
         }
         if (ok) umma_commit(&bars[L::bAcc]);
       }
@@ -432,10 +443,9 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
     const int half = warp >> 2;
     const int row = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_tm = tmem + lane_base + half * 64;
-    const uint32_t d_tm = s_tm + 128;
     const uint64_t sc2 = f32x2_pack(p.scale_log2, p.scale_log2);
-    uint32_t ns = 0, n = 0, slot = 0, nd_phase = 0;
+    uint32_t n = 0, slot = 0, nd_phase = 0;
+    uint32_t ns = 0;  // bit b: the phase of buffer b's next scores (both halves' uses of it change it)
     int4 it;
     while (next_item(&it, 53 + half)) {
       const int steps = steps_of(it), per = kKv ? n_tiles(it) - it.z : steps;
@@ -447,11 +457,15 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
         mine.x *= 1.4426950408889634f;
       }
       for (int i = 0; i < steps; ++i, ++slot) {
+        const uint32_t buf = (2 * i + half) % L::kBufs;
         const int yt = kKv ? it.z + i % per : i;
         const uint32_t st = (2 * slot + half) % L::kStages;
-        if (!warp_wait(&bars[L::bS + half], ns & 1, abort_flag, kDevTimeoutSoftmax, 20 + half, (int)ns, i)) goto done;
-        ++ns;
+        const uint32_t phase = (ns >> buf) & 1;
+        ns ^= 1u << buf;
+        if constexpr (L::kBufs == 3) ns ^= 1u << ((2 * i + 1 - half) % 3);  // the other half's use
+        if (!warp_wait(&bars[L::bS + buf], phase, abort_flag, kDevTimeoutSoftmax, 20 + half, (int)slot, i)) goto done;
         tc_fence_after();
+        const uint32_t s_tm = tmem + lane_base + buf * 128, d_tm = s_tm + 64;
         // Columns kept: kv: query c >= key row on the diagonal, inside the sequence; q: key c <= query row.
         int lo = 0, hi = 128;
         if (kKv) {
@@ -529,7 +543,7 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
         if (warp_all) tile(std::false_type{});
         else tile(std::true_type{});
         tmem_wait_st();
-        warp_arrive_tc(&bars[L::bP + half]);
+        warp_arrive_tc(&bars[L::bP + buf]);
       }
       // ---- epilogue: kv: this half writes dv (0) or dk (1); q: its half of dq's columns
       if (!warp_wait(&bars[L::bAcc], n & 1, abort_flag, kDevTimeoutSoftmax, 24 + half, (int)n)) goto done;
@@ -540,7 +554,7 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
         const bool one = kKv && half == 0;
         const SeqView& out = one ? p.out1 : p.out2;
         const int c0 = kKv ? 0 : half * (D / 2);
-        const uint32_t acc = tmem + lane_base + 256 + (one ? 0 : D) + c0;
+        const uint32_t acc = tmem + lane_base + (one ? L::kAcc1 : L::kAcc2) + c0;
         const float f = one ? 1.f : p.scale;
         T* dst = static_cast<T*>(out.ptr) + it.w * out.sh + tok * out.st + c0;
         #pragma unroll
