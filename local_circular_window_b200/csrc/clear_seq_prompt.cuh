@@ -13,8 +13,10 @@
 //   warp 8           TMA: Q tiles, then K and V tiles through one ring (K0 K1 V0 K2 V1 ...)
 //   warp 9           one thread issues the products: S = Q K^T into TMEM, then O += P V with P from TMEM
 //   warp 11          finds the block's items, ahead of the others, through a small ring
-// TMEM: S of A and B at columns 0 and 128 (P overwrites S, 16-bit, two values a column: the 32 keys of each
-// 32 columns go into the first 16), O at 256 and 256 + d.
+// TMEM: two buffers of S (three at d = 64) of 128 columns, then O of A and of B. P overwrites S, 16-bit, two values a
+// column: the 32 keys of each 32 columns go into the first 16. The tiles of S take the buffers in turn, in the order A0, B0,
+// A1, B1, ... (A0, A1, ... for an item without tile B); the next one's product is issued behind the P V that
+// frees its buffer.
 // While one tile's softmax runs, the other tile's products do: the issuer alternates A, B. (An issuer for each
 // tile mixes the two tiles' products in the tensor pipe: 1782 us in place of 1416 at 16896 tokens and 24 heads.)
 //
@@ -137,6 +139,9 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&x)[32]) {
 
 template <int D>
 struct PromptLayout {
+  static constexpr int kBufs = D == 128 ? 2 : 3;
+  static constexpr int kO = kBufs * 128;                 // O of tile A; tile B's follows
+  static_assert(kO + 2 * D <= 512, "tensor memory");
   static constexpr int kTileBytes = 128 * D * 2;
   static constexpr int kBlock = 128 * 128;               // 128 rows x 64 elements, 128-byte swizzle
   static constexpr int kStages = D == 128 ? 5 : 8;       // ring of K and V tiles
@@ -145,9 +150,11 @@ struct PromptLayout {
   static constexpr int kBars = kRing + kStages * kTileBytes;
   static constexpr int bQFull = 0, bQEmpty = 1;
   static constexpr int bFull = 2, bEmpty = bFull + kStages;
-  static constexpr int bS = bEmpty + kStages;            // + tile: S written
-  static constexpr int bP = bS + 2;                      // + tile * kPrParts + part: P's part written (and O rescaled)
-  static constexpr int bO = bP + 2 * kPrParts;           // + tile: the item's last P V done
+  // A barrier for each buffer and query tile: a warpgroup sees only the phases that are its own, and so is never more than one
+  // behind, which is what waiting by parity needs.
+  static constexpr int bS = bEmpty + kStages;            // + 2 * buffer + tile: S written
+  static constexpr int bP = bS + 2 * kBufs;              // + buffer * kPrParts + part: P's part written (and O rescaled)
+  static constexpr int bO = bP + kBufs * kPrParts;       // + tile: a P V done
   static constexpr int bItemFull = bO + 2, bItemEmpty = bItemFull + kPrItems;
   static constexpr int bDrain = bItemEmpty + kPrItems;
   static constexpr int kNumBars = bDrain + 1;
@@ -192,11 +199,13 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
       mbar_init(&bars[L::bFull + s], 1);
       mbar_init(&bars[L::bEmpty + s], 1);
     }
-    for (int h = 0; h < 2; ++h) {
-      mbar_init(&bars[L::bS + h], 1);
-      for (int i = 0; i < kPrParts; ++i) mbar_init(&bars[L::bP + h * kPrParts + i], 4);
-      mbar_init(&bars[L::bO + h], 1);
+    for (int b = 0; b < L::kBufs; ++b) {
+      mbar_init(&bars[L::bS + 2 * b], 1);
+      mbar_init(&bars[L::bS + 2 * b + 1], 1);
+      for (int i = 0; i < kPrParts; ++i) mbar_init(&bars[L::bP + b * kPrParts + i], 4);
     }
+    mbar_init(&bars[L::bO], 1);
+    mbar_init(&bars[L::bO + 1], 1);
     for (int i = 0; i < kPrItems; ++i) {
       mbar_init(&bars[L::bItemFull + i], 1);
       mbar_init(&bars[L::bItemEmpty + i], 10);  // the loader, the issuer, eight softmax warps
@@ -276,84 +285,104 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
     const uint64_t kdesc = smem_desc_sw128(smem_u32(smem + L::kRing), 16, 1024);
     const uint64_t vdesc = smem_desc_sw128(smem_u32(smem + L::kRing), L::kBlock, 1024);
     int4 it;
-    uint32_t n = 0, np0 = 0, np1 = 0;
-    uint32_t stage = 0, phase = 0;  // of the next tile in the ring
+    uint32_t n = 0;
+    uint32_t uses = 0;           // bit b: whether buffer b has had an odd number of uses in earlier items
+    uint32_t base = 0, wrap = 0; // stage and phase of the item's first tile in the ring
     bool ok = true;
+    // A place in the ring.
+    struct Place {
+      uint32_t stage, phase;
+      __device__ __forceinline__ void advance(uint32_t k) {
+        stage += k;
+        if (stage >= L::kStages) {
+          stage -= L::kStages;
+          phase ^= 1;
+        }
+      }
+    };
     while (ok && next_item(&it, 41)) {
+      const bool two = it.y > 128;
+      const int nA = it.z + 1, nB = two ? it.z + 2 : 0;
+      const int tiles = two ? nB : nA, total = nA + nB;
       if (elect_one()) {
-        const bool two = it.y > 128;
-        const int nA = it.z + 1, nB = two ? it.z + 2 : 0;
-        const int tiles = two ? nB : nA;
-        const auto advance = [&]() {
-          if (++stage == L::kStages) {
-            stage = 0;
-            phase ^= 1;
+        // The next tile of S to be computed (key tile jq of query tile hq), and of P to be used. Ring order:
+        // K0, K1, V0, K2, V1, ..., V(tiles-1).
+        int jq = 0, hq = 0, gq = 0, jp = 0, hp = 0;
+        Place kp{base, wrap}, vp{base, wrap};
+        vp.advance(tiles == 1 ? 1 : 2);
+        const auto next = [&](int& j, int& h) {  // returns whether key tile j is done with
+          if (two && h == 0) {
+            h = 1;
+            return false;
           }
+          ++j;
+          h = two && j >= nA ? 1 : 0;
+          return true;
         };
-        const auto full = [&](uint32_t st, uint32_t ph) {
-          ok = ok && seq_wait(&bars[L::bFull + st], ph, abort_flag, kDevTimeoutMma, 11, (int)n, (int)st);
+        const auto full = [&](const Place& x) {
+          ok = ok && seq_wait(&bars[L::bFull + x.stage], x.phase, abort_flag, kDevTimeoutMma, 11, (int)n, (int)x.stage);
         };
-        const auto qk = [&](int h, uint32_t st) {
-          const uint64_t kd = kdesc + (uint64_t)((st * L::kTileBytes) >> 4);
-          const uint64_t qd = qdesc + (uint64_t)((h * L::kTileBytes) >> 4);
+        const auto qk = [&](int b) {
+          full(kp);
+          if (!ok) return;
+          const uint64_t kd = kdesc + (uint64_t)((kp.stage * L::kTileBytes) >> 4);
+          const uint64_t qd = qdesc + (uint64_t)((hq * L::kTileBytes) >> 4);
           #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4;
-            umma_ss(tmem + h * 128, qd + off, kd + off, idesc_qk, kk > 0);
+            umma_ss(tmem + b * 128, qd + off, kd + off, idesc_qk, kk > 0);
           }
-          umma_commit(&bars[L::bS + h]);
+          umma_commit(&bars[L::bS + 2 * b + hq]);
+          const uint32_t st = kp.stage;
+          const int j = jq;
+          if (next(jq, hq)) {
+            umma_commit(&bars[L::bEmpty + st]);
+            kp.advance(j == 0 ? 1 : 2);
+          }
+          if (++gq == total) umma_commit(&bars[L::bQEmpty]);
         };
-        const auto pv = [&](int h, uint32_t st, uint32_t ph, bool first) {
-          const uint64_t vd = vdesc + (uint64_t)((st * L::kTileBytes) >> 4);
+        const auto pv = [&](int b, uint32_t phase) {
+          full(vp);
+          const uint64_t vd = vdesc + (uint64_t)((vp.stage * L::kTileBytes) >> 4);
+          const uint32_t o_tm = tmem + L::kO + hp * D;
           #pragma unroll
           for (int i = 0; i < kPrParts; ++i) {
-            ok = ok && seq_wait(&bars[L::bP + h * kPrParts + i], ph & 1, abort_flag, kDevTimeoutMma, 13 + h, (int)n, (int)st);
+            ok = ok && seq_wait(&bars[L::bP + b * kPrParts + i], phase, abort_flag, kDevTimeoutMma, 13, (int)n, jp);
             if (!ok) return;
             tc_fence_after();
             #pragma unroll
             for (int kk = i * (8 / kPrParts); kk < (i + 1) * (8 / kPrParts); ++kk)
-              umma_ts(tmem + 256 + h * D, tmem + h * 128 + (kk >> 1) * 32 + (kk & 1) * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv,
-                      (!first || kk > 0) ? 1u : 0u);
+              umma_ts(o_tm, tmem + b * 128 + (kk >> 1) * 32 + (kk & 1) * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv,
+                      (jp > 0 || kk > 0) ? 1u : 0u);
+          }
+          umma_commit(&bars[L::bO + hp]);
+          const uint32_t st = vp.stage;
+          if (next(jp, hp)) {
+            umma_commit(&bars[L::bEmpty + st]);
+            vp.advance(jp == tiles - 1 ? 1 : 2);
           }
         };
         ok = seq_wait(&bars[L::bQFull], n & 1, abort_flag, kDevTimeoutMma, 10, (int)n);
-        // Ring order: K0, K1, V0, K2, V1, ..., V(tiles-1)
-        full(stage, phase);
-        if (ok) {
-          qk(0, stage);
-          if (two) qk(1, stage);
-          umma_commit(&bars[L::bEmpty + stage]);
-          if (tiles == 1) umma_commit(&bars[L::bQEmpty]);
-          advance();
-        }
-        for (int j = 0; j < tiles && ok; ++j) {
-          const uint32_t kst = stage, kph = phase;
-          if (j + 1 < tiles) {
-            full(kst, kph);
-            advance();
+        #pragma unroll
+        for (int b = 0; b < L::kBufs; ++b)
+          if (b < total && ok) qk(b);
+        uint32_t flip = 0;
+        for (int g = 0; g < total && ok; g += L::kBufs) {
+          #pragma unroll
+          for (int b = 0; b < L::kBufs; ++b) {
+            if (g + b < total && ok) {
+              pv(b, ((uses >> b) & 1) ^ flip);
+              if (ok && gq < total) qk(b);
+            }
           }
-          full(stage, phase);
-          if (!ok) break;
-          if (j < nA) {
-            pv(0, stage, np0++, j == 0);
-            if (!ok) break;
-            if (j == nA - 1) umma_commit(&bars[L::bO]);
-            else qk(0, kst);
-          }
-          if (j < nB) {
-            pv(1, stage, np1++, j == 0);
-            if (!ok) break;
-          }
-          umma_commit(&bars[L::bEmpty + stage]);
-          if (j == nB - 1) umma_commit(&bars[L::bO + 1]);
-          if (j + 1 < nB) qk(1, kst);
-          if (j + 1 < tiles) {
-            umma_commit(&bars[L::bEmpty + kst]);
-            if (j + 2 == tiles) umma_commit(&bars[L::bQEmpty]);  // the last product with Q has been issued
-          }
-          advance();
+          flip ^= 1;
         }
       }
+      #pragma unroll
+      for (int b = 0; b < L::kBufs; ++b) uses ^= (((total - b + L::kBufs - 1) / L::kBufs) & 1) << b;
+      base += 2 * tiles;
+      wrap ^= (base / L::kStages) & 1;
+      base %= L::kStages;
       __syncwarp();
       ok = __all_sync(0xffffffffu, ok);
       ++n;
@@ -408,21 +437,26 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
     const int half = warp >> 2;
     const int row = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_tm = tmem + lane_base + half * 128;
-    const uint32_t o_tm = tmem + lane_base + 256 + half * D;
-    uint32_t ns = 0, no = 0, tiles_before = 0;  // key tiles of earlier items
+    const uint32_t o_tm = tmem + lane_base + L::kO + half * D;
+    uint32_t no = 0, tiles_before = 0;  // P V products of this query tile and key tiles of earlier items
+    uint32_t ns = 0;                    // bit b: the phase of buffer b's next S for this query tile
     int4 it;
     while (next_item(&it, 42 + half)) {
       const uint32_t ring0 = 2 * tiles_before;  // the item's first place in the ring
       const int all_tiles = it.z + (it.y > 128 ? 2 : 1);
       tiles_before += all_tiles;
-      if (half == 1 && it.y <= 128) continue;  // no tile B
+      const bool two = it.y > 128;
+      const int nA = it.z + 1;
+      if (half == 1 && !two) continue;  // no tile B
       const int tiles = it.z + 1 + half;
       const bool valid = half * 128 + row < it.y;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < tiles; ++j) {
-        if (!warp_wait(&bars[L::bS + half], ns & 1, abort_flag, kDevTimeoutSoftmax, 20 + half, (int)ns, j)) goto done;
-        ++ns;
+        const int g = !two ? j : j < nA ? 2 * j + half : 2 * nA;  // the tile's place in the order of S
+        const uint32_t buf = g % L::kBufs;
+        const uint32_t s_tm = tmem + lane_base + buf * 128;
+        if (!warp_wait(&bars[L::bS + 2 * buf + half], (ns >> buf) & 1, abort_flag, kDevTimeoutSoftmax, 20 + half, g, j)) goto done;
+        ns ^= 1u << buf;
         tc_fence_after();
         // The exponentials of the first 64 keys are taken with the maximum in use while the true maximum of all 128 is
         // still being found: the comparisons run in the special-function unit's shadow. Only where the
@@ -482,7 +516,9 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
           const float a = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
           m = m_new;
           l *= a;
-          if (j > 0) {  // this tile's S was issued behind the last P V: O is at rest
+          if (j > 0) {  // once the last P V is done
+            if (!warp_wait(&bars[L::bO + half], (no + j - 1) & 1, abort_flag, kDevTimeoutSoftmax, 22 + half, (int)no, j)) goto done;
+            tc_fence_after();
             #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               tmem_ld32(o_tm + c * 32, a0);
@@ -505,7 +541,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
         }
         const auto hand_over = [&](int part) {
           tmem_wait_st();
-          warp_arrive_tc(&bars[L::bP + half * kPrParts + part]);
+          warp_arrive_tc(&bars[L::bP + buf * kPrParts + part]);
         };
         if (diagonal && it.y < (half + 1) * 128) {  // the tile reaches behind the sequence's end: clear its value rows there
           const uint32_t v = ring0 + (j == all_tiles - 1 ? 2 * all_tiles - 1 : 2 * j + 2), st = v % L::kStages;
@@ -529,8 +565,8 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
         l += f32x2_lo(sum[0]) + f32x2_hi(sum[0]);
       }
       // ---- epilogue
-      if (!warp_wait(&bars[L::bO + half], no & 1, abort_flag, kDevTimeoutSoftmax, 24 + half, (int)no)) goto done;
-      ++no;
+      no += tiles;
+      if (!warp_wait(&bars[L::bO + half], (no - 1) & 1, abort_flag, kDevTimeoutSoftmax, 24 + half, (int)no)) goto done;
       tc_fence_after();
       {
         const float inv = l == 0.f ? 0.f : 1.f / l;

@@ -445,7 +445,10 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint64_t sc2 = f32x2_pack(p.scale_log2, p.scale_log2);
     uint32_t n = 0, slot = 0, nd_phase = 0;
-    uint32_t ns = 0;  // bit b: the phase of buffer b's next scores (both halves' uses of it change it)
+    // Bit b: the phase of buffer b's next scores; both halves' uses of it change it. Waiting by parity is sound: the buffer's last
+    // use is three halves back (within an item) or before the accumulators' last product (earlier items), and this
+    // warpgroup has seen something later than that: its own last half, or the item's end.
+    uint32_t ns = 0;
     int4 it;
     while (next_item(&it, 53 + half)) {
       const int steps = steps_of(it), per = kKv ? n_tiles(it) - it.z : steps;
