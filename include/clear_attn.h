@@ -499,7 +499,8 @@ CLEAR_API clear_status_t clear_attn_prompt_fwd(const clear_seq_params_t* params,
                                                const clear_seq_view_t* v, const clear_seq_view_t* o, float* lse,
                                                void* stream);
 
-/* Workspace bytes of clear_attn_prompt_bwd (two fp32 per query row and head). */
+/* Workspace bytes of clear_attn_prompt_bwd: two fp32 per query row and head and, where few key/value heads leave the GPU
+ * idle, fp32 partial sums of dk and dv (at most about 77 MB). */
 CLEAR_API size_t clear_attn_prompt_bwd_workspace_size(const clear_seq_params_t* params, clear_status_t* status);
 
 /*

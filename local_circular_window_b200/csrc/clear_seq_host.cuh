@@ -190,6 +190,30 @@ clear_status_t launch_prompt_fwd(const clear_seq_params_t* sp, const SeqView& q,
   return cudaGetLastError() == cudaSuccess ? CLEAR_OK : CLEAR_ERR_CUDA;
 }
 
+// Parts that a group's heads are split into for dK and dV: enough that every SM gets two items, where the heads allow it. One
+// kv head of 16 query heads on 2048 tokens has 16 items for 148 SMs without. By the parameters alone: the workspace has room
+// for the parts' fp32 sums, at most about 75000 rows in all of each of dK and dV.
+int bwd_parts(const clear_seq_params_t* p) {
+  constexpr long long kWanted = 2 * 148;
+  const long long items = (((long long)p->n_tok + 127) / 128) * p->kv_heads;
+  const long long group = p->q_heads / p->kv_heads;
+  const long long parts = (kWanted + items - 1) / items;
+  return (int)(parts < 1 ? 1 : parts > group ? group : parts);
+}
+
+struct PromptBwdWorkspace {
+  size_t part1_off, part2_off, total;
+};
+PromptBwdWorkspace prompt_bwd_workspace_layout(const clear_seq_params_t* p) {
+  PromptBwdWorkspace w;
+  const int parts = bwd_parts(p);
+  const size_t sums = parts > 1 ? (size_t)parts * p->kv_heads * p->n_tok * p->d * sizeof(float) : 0;
+  w.part1_off = align256((size_t)p->q_heads * p->n_tok * sizeof(float2));
+  w.part2_off = w.part1_off + align256(sums);
+  w.total = w.part2_off + align256(sums);
+  return w;
+}
+
 template <typename E, int D>
 clear_status_t launch_prompt_bwd(const clear_seq_params_t* sp, const SeqView& q, const SeqView& k, const SeqView& v, const SeqView& g,
                                  const SeqView& dq, const SeqView& dk, const SeqView& dv, const SeqStatsParams& st, SeqBwdParams p,
@@ -215,7 +239,12 @@ clear_status_t launch_prompt_bwd(const clear_seq_params_t* sp, const SeqView& q,
   if (cudaGetLastError() != cudaSuccess) return CLEAR_ERR_CUDA;
   p.out1 = dv;
   p.out2 = dk;
-  clear_seq_prompt_bwd_kernel<E, D, true><<<prompt_blocks(sp, 128, sp->kv_heads, num_sms), kPrThreads, LK::kAlloc, stream>>>(mk, mv, sq, sg, p);
+  clear_seq_prompt_bwd_kernel<E, D, true><<<prompt_blocks(sp, 128, sp->kv_heads * p.parts, num_sms), kPrThreads, LK::kAlloc, stream>>>(mk, mv, sq, sg, p);
+  if (cudaGetLastError() != cudaSuccess) return CLEAR_ERR_CUDA;
+  if (p.parts > 1) {
+    const long long threads = 2ll * sp->kv_heads * sp->n_tok * (D / 8);
+    clear_seq_bwd_join_kernel<E, D><<<(unsigned)((threads + kStatsThreads - 1) / kStatsThreads), kStatsThreads, 0, stream>>>(p);
+  }
   return cudaGetLastError() == cudaSuccess ? CLEAR_OK : CLEAR_ERR_CUDA;
 }
 
@@ -339,7 +368,7 @@ clear_status_t clear_attn_prompt_fwd(const clear_seq_params_t* params, const int
 size_t clear_attn_prompt_bwd_workspace_size(const clear_seq_params_t* params, clear_status_t* status) {
   const clear_status_t st = check_seq_params(params);
   if (status) *status = st;
-  return st == CLEAR_OK ? align256((size_t)params->q_heads * params->n_tok * sizeof(float2)) : 0;
+  return st == CLEAR_OK ? prompt_bwd_workspace_layout(params).total : 0;
 }
 
 clear_status_t clear_attn_prompt_bwd(const clear_seq_params_t* params, const int* seq_start, const clear_seq_view_t* q,
@@ -356,7 +385,7 @@ clear_status_t clear_attn_prompt_bwd(const clear_seq_params_t* params, const int
     const bool kv = i == 1 || i == 2 || i == 6 || i == 7;
     if ((st = check_seq_view(views[i], kv ? params->kv_heads : params->q_heads, params->n_tok, params->d, &w[i])) != CLEAR_OK) return st;
   }
-  if (!workspace || workspace_bytes < clear_attn_prompt_bwd_workspace_size(params, nullptr) ||
+  if (!workspace || workspace_bytes < prompt_bwd_workspace_layout(params).total ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return CLEAR_ERR_WORKSPACE;
   // The row statistics take one thread per 8 elements of o; their grid must fit.
@@ -370,6 +399,10 @@ clear_status_t clear_attn_prompt_bwd(const clear_seq_params_t* params, const int
   sp.stats = static_cast<float2*>(workspace);
   SeqBwdParams p{};
   p.stats = sp.stats;
+  const PromptBwdWorkspace wl = prompt_bwd_workspace_layout(params);
+  p.parts = bwd_parts(params);
+  p.part1 = reinterpret_cast<float*>(static_cast<char*>(workspace) + wl.part1_off);
+  p.part2 = reinterpret_cast<float*>(static_cast<char*>(workspace) + wl.part2_off);
   p.seq_start = sp.seq_start = seq_start;
   p.n_seq = sp.n_seq = params->n_seq;
   p.n_tok = sp.n_tok = params->n_tok;

@@ -9,7 +9,8 @@
 //   kv      one item per 128-key tile and kv head: K and V stay, the group's Q and dO stream past
 // S and dP are computed in both, seven products in place of five: the price of writing every gradient
 // once, in a fixed order. (Adding dQ up with atomics would need 64 KB of fp32 traffic per tile and
-// would change the result from run to run; grouped heads' dK and dV add up in TMEM.)
+// would change the result from run to run; grouped heads' dK and dV add up in TMEM.) Where few kv heads make few
+// kv items, the group's heads are split into parts, whose fp32 sums a last kernel adds up in order.
 //
 // Both are one kernel. X1, X2 are the tiles that stay, Y1, Y2 the ones that stream (128 rows each,
 // used as halves of 64 rows):
@@ -50,6 +51,9 @@ namespace clear {
 
 struct SeqBwdParams {
   SeqView out1, out2;    // kv: dv, dk; q: -, dq
+  // kv with parts > 1: each item takes one part of the group's heads and writes fp32 sums [parts][kv_heads][n_tok][d].
+  int parts;
+  float *part1, *part2;
   float2* stats;         // [q_heads, n_tok]: (-lse, -D)
   const int* seq_start;
   int n_seq, n_tok, q_heads, kv_heads, group;
@@ -226,7 +230,16 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
   // Streamed tiles of an item: kv: for each head of the group the query tiles from the key tile on;
   // q: the key tiles up to the query tile.
   const auto n_tiles = [](const int4& it) { return (it.y + 127) >> 7; };
-  const auto steps_of = [&](const int4& it) { return kKv ? p.group * (n_tiles(it) - it.z) : it.z + 1; };
+  // An item's head: q: the query head; kv: kv head * parts + part, with the group's heads [h_first, h_first + h_count).
+  const auto h_first = [&](const int4& it) {
+    const int hk = it.w / p.parts, part = it.w - hk * p.parts;
+    return hk * p.group + part * p.group / p.parts;
+  };
+  const auto h_count = [&](const int4& it) {
+    const int part = it.w % p.parts;
+    return (part + 1) * p.group / p.parts - part * p.group / p.parts;
+  };
+  const auto steps_of = [&](const int4& it) { return kKv ? h_count(it) * (n_tiles(it) - it.z) : it.z + 1; };
 
   if (warp == 8) {
     // ------------------------------------------------------------------ loader
@@ -236,12 +249,13 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
     bool ok = true;
     while (ok && next_item(&it, 50)) {
       if (lane == 0) {
-        const int steps = steps_of(it), per = kKv ? n_tiles(it) - it.z : steps;
+        const int steps = steps_of(it), per = kKv ? n_tiles(it) - it.z : steps, head0 = kKv ? h_first(it) : it.w / p.group;
         ok = seq_wait(&bars[L::bXEmpty], (n & 1) ^ 1, abort_flag, kDevTimeoutTmaEmpty, 1, (int)n);
         if (ok) {
           mbar_arrive_expect_tx(&bars[L::bXFull], 2 * L::kTileBytes);
-          load_seq_tile<D>(smem + L::kX, &tm_x1, &bars[L::bXFull], it.x + it.z * 128, it.w);
-          load_seq_tile<D>(smem + L::kX + L::kTileBytes, &tm_x2, &bars[L::bXFull], it.x + it.z * 128, it.w);
+          const int head = kKv ? it.w / p.parts : it.w;
+          load_seq_tile<D>(smem + L::kX, &tm_x1, &bars[L::bXFull], it.x + it.z * 128, head);
+          load_seq_tile<D>(smem + L::kX + L::kTileBytes, &tm_x2, &bars[L::bXFull], it.x + it.z * 128, head);
           ++x_loads;
         }
         for (int i = 0; i < 2 * steps && ok; ++i) {  // halves
@@ -249,7 +263,7 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
           ok = seq_wait(&bars[L::bYEmpty + s], ((slot / L::kStages) & 1) ^ 1, abort_flag, kDevTimeoutTmaEmpty, 2, (int)n, i);
           if (!ok) break;
           const int tile = kKv ? it.z + (i >> 1) % per : i >> 1;
-          const int head = kKv ? it.w * p.group + (i >> 1) / per : it.w / p.group;
+          const int head = kKv ? head0 + (i >> 1) / per : head0;
           const int tok = it.x + tile * 128 + (i & 1) * 64;
           uint8_t* dst = smem + L::kY + s * L::kStageBytes;
           mbar_arrive_expect_tx(&bars[L::bYFull + s], L::kStageBytes);
@@ -372,7 +386,7 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
     // ------------------------------------------------------------------ item finder
     regs_dec<kPrRegsLow>();
     TileList list;
-    const int heads = kKv ? p.kv_heads : p.q_heads;
+    const int heads = kKv ? p.kv_heads * p.parts : p.q_heads;
     const long long total = list.init(p.seq_start, p.n_seq, p.n_tok, 128) * heads;
     if (kKv && blockIdx.x == 0) {
       for (int s = lane; s < p.n_seq; s += 32) {
@@ -413,10 +427,10 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
       uint32_t slot = 0;
       bool ok = true;
       while (ok && next_item(&it, 52)) {
-        const int steps = steps_of(it), per = n_tiles(it) - it.z;
+        const int steps = steps_of(it), per = n_tiles(it) - it.z, head0 = h_first(it);
         for (int i = 0; i < 2 * steps; ++i, ++slot) {
           const int t0 = (it.z + (i >> 1) % per) * 128 + (i & 1) * 64;
-          const float2* src = p.stats + (long long)(it.w * p.group + (i >> 1) / per) * p.n_tok + it.x + t0;
+          const float2* src = p.stats + (long long)(head0 + (i >> 1) / per) * p.n_tok + it.x + t0;
           float2 v[2];
           #pragma unroll
           for (int e = 0; e < 2; ++e) v[e] = t0 + e * 32 + lane < it.y ? src[e * 32 + lane] : make_float2(0.f, 0.f);
@@ -559,13 +573,20 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
         const int c0 = kKv ? 0 : half * (D / 2);
         const uint32_t acc = tmem + lane_base + (one ? L::kAcc1 : L::kAcc2) + c0;
         const float f = one ? 1.f : p.scale;
-        T* dst = static_cast<T*>(out.ptr) + it.w * out.sh + tok * out.st + c0;
+        const bool sums = kKv && p.parts > 1;
+        const int hk = kKv ? it.w / p.parts : it.w;
+        T* dst = static_cast<T*>(out.ptr) + hk * out.sh + tok * out.st + c0;
+        float* part = sums ? (one ? p.part1 : p.part2) + (((long long)(it.w % p.parts) * p.kv_heads + hk) * p.n_tok + tok) * D : nullptr;
         #pragma unroll
         for (int c = 0; c < kCols / 32; ++c) {
           uint32_t ov[32];
           tmem_ld32(acc + c * 32, ov);
-          tmem_wait_ld();
-          if (valid) {
+          tmem_wait_ld(ov);
+          if (valid && sums) {
+            #pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<uint4*>(part)[c * 8 + e] = make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+          } else if (valid) {
             #pragma unroll
             for (int e = 0; e < 4; ++e) {
               uint32_t w[4];
@@ -585,6 +606,47 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// Adds up the parts of dV and dK in their order: a thread takes 8 elements of one row of one of the two.
+template <typename E, int D>
+__global__ void __launch_bounds__(kStatsThreads) clear_seq_bwd_join_kernel(const __grid_constant__ SeqBwdParams p) {
+  using T = typename E::type;
+  const long long rows = (long long)p.kv_heads * p.n_tok;
+  const long long i = (long long)blockIdx.x * kStatsThreads + threadIdx.x;
+  const int c = (int)(i % (D / 8));
+  const long long r = i / (D / 8);
+  if (r >= 2 * rows) return;
+  const bool one = r < rows;
+  const long long row = one ? r : r - rows;
+  const int h = (int)(row / p.n_tok);
+  const long long t = row - (long long)h * p.n_tok;
+  // Only rows that belong to a sequence have been summed: find it, as a token's sequence is found for the cache.
+  int lo = 0, n = p.n_seq;
+  while (n > 1) {
+    const int m = n / 2;
+    if (__ldg(p.seq_start + lo + m) <= t) {
+      lo += m;
+      n -= m;
+    } else {
+      n = m;
+    }
+  }
+  int first, len;
+  seq_range(p.seq_start, p.n_tok, lo, &first, &len);
+  if (t < first || t >= first + len) return;
+  const float* src = (one ? p.part1 : p.part2) + (row * D + c * 8);
+  float y[8] = {};
+  for (int k = 0; k < p.parts; ++k) {
+    const float4 a = *reinterpret_cast<const float4*>(src + k * rows * D), b = *reinterpret_cast<const float4*>(src + k * rows * D + 4);
+    y[0] += a.x; y[1] += a.y; y[2] += a.z; y[3] += a.w;
+    y[4] += b.x; y[5] += b.y; y[6] += b.z; y[7] += b.w;
+  }
+  const float f = one ? 1.f : p.scale;
+  const SeqView& out = one ? p.out1 : p.out2;
+  T* dst = static_cast<T*>(out.ptr) + h * out.sh + t * out.st;
+  reinterpret_cast<uint4*>(dst)[c] =
+      make_uint4(E::pack(y[0] * f, y[1] * f), E::pack(y[2] * f, y[3] * f), E::pack(y[4] * f, y[5] * f), E::pack(y[6] * f, y[7] * f));
 }
 
 }  // namespace clear

@@ -51,6 +51,8 @@ CASES = [  # lens, q_heads, kv_heads, d, dtype
     ([3] * 50 + [300, 0, 0, 2], 2, 2, 64, torch.float16),
     ([0, 0, 5], 1, 1, 128, torch.float16),
     ([1153], 2, 1, 128, torch.bfloat16),
+    ([300, 0, 70], 16, 1, 64, torch.bfloat16),   # many heads to one: the group is split and joined
+    ([140], 7, 1, 128, torch.float16),
 ]
 
 
