@@ -20,6 +20,11 @@
 // While one tile's softmax runs, the other tile's products do: the issuer alternates A, B. (An issuer for each
 // tile mixes the two tiles' products in the tensor pipe: 1782 us in place of 1416 at 16896 tokens and 24 heads.)
 //
+// Short batches (kSplit). With two query tiles an item, a few heads of a few thousand tokens are too few items for 148 SMs,
+// and the last tiles' items bound the whole. There an item is one query tile: "tile A" takes its even key tiles and
+// "tile B" the odd ones, and the two halves' (m, l, O) are joined at the end, O_A and O_B lying in the same lanes of TMEM.
+// Every key tile then serves 128 rows instead of 256.
+//
 // Items are ordered by their number of key tiles, the longest first, over all sequences, and dealt to
 // the blocks back and forth, so that every block gets about the same work. Heads of one group follow
 // one another: they read the same keys and values, from L2.
@@ -157,7 +162,8 @@ struct PromptLayout {
   static constexpr int bO = bP + kBufs * kPrParts;       // + tile: a P V done
   static constexpr int bItemFull = bO + 2, bItemEmpty = bItemFull + kPrItems;
   static constexpr int bDrain = bItemEmpty + kPrItems;
-  static constexpr int kNumBars = bDrain + 1;
+  static constexpr int bJoin = bDrain + 1, bJoined = bDrain + 2;    // kSplit: (m, l) of both halves written; O of both read
+  static constexpr int kNumBars = bDrain + 3;
   static constexpr int kItems = (kBars + kNumBars * 8 + 15) & ~15;  // int4[kPrItems]
   static constexpr int kMisc = kItems + kPrItems * 16;
   static constexpr int kAlloc = kMisc + 16 + 1024;
@@ -178,12 +184,13 @@ __device__ __forceinline__ void load_seq_tile(uint8_t* dst, const CUtensorMap* m
 }
 
 // An item as the ring carries it: {first token of tile A, query rows left from there, tile A's number, head}.
-template <typename E, int D>
+template <typename E, int D, bool kSplit>
 __global__ void __launch_bounds__(kPrThreads, 1)
 clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ SeqPromptParams p) {
   using L = PromptLayout<D>;
   using T = typename E::type;
+  constexpr int kRows = kSplit ? 128 : 256;  // query rows of an item
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
@@ -211,6 +218,8 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
       mbar_init(&bars[L::bItemEmpty + i], 10);  // the loader, the issuer, eight softmax warps
     }
     mbar_init(&bars[L::bDrain], 1);
+    mbar_init(&bars[L::bJoin], 8);
+    mbar_init(&bars[L::bJoined], 8);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -244,7 +253,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
     while (ok && next_item(&it, 40)) {
       if (lane == 0) {
         const int hk = it.w / p.group;
-        const bool two = it.y > 128;
+        const bool two = !kSplit && it.y > 128;
         const int tiles = it.z + (two ? 2 : 1);  // key tiles of the item
         const int seq0 = it.x - it.z * 128;      // the sequence's first token
         ok = seq_wait(&bars[L::bQEmpty], (n & 1) ^ 1, abort_flag, kDevTimeoutTmaEmpty, 1, (int)n);
@@ -301,7 +310,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
       }
     };
     while (ok && next_item(&it, 41)) {
-      const bool two = it.y > 128;
+      const bool two = !kSplit && it.y > 128;
       const int nA = it.z + 1, nB = two ? it.z + 2 : 0;
       const int tiles = two ? nB : nA, total = nA + nB;
       if (elect_one()) {
@@ -311,6 +320,11 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
         Place kp{base, wrap}, vp{base, wrap};
         vp.advance(tiles == 1 ? 1 : 2);
         const auto next = [&](int& j, int& h) {  // returns whether key tile j is done with
+          if (kSplit) {
+            ++j;
+            h ^= 1;
+            return true;
+          }
           if (two && h == 0) {
             h = 1;
             return false;
@@ -326,7 +340,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
           full(kp);
           if (!ok) return;
           const uint64_t kd = kdesc + (uint64_t)((kp.stage * L::kTileBytes) >> 4);
-          const uint64_t qd = qdesc + (uint64_t)((hq * L::kTileBytes) >> 4);
+          const uint64_t qd = qdesc + (uint64_t)((kSplit ? 0 : hq * L::kTileBytes) >> 4);
           #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4;
@@ -353,7 +367,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
             #pragma unroll
             for (int kk = i * (8 / kPrParts); kk < (i + 1) * (8 / kPrParts); ++kk)
               umma_ts(o_tm, tmem + b * 128 + (kk >> 1) * 32 + (kk & 1) * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv,
-                      (jp > 0 || kk > 0) ? 1u : 0u);
+                      (jp > (kSplit ? hp : 0) || kk > 0) ? 1u : 0u);
           }
           umma_commit(&bars[L::bO + hp]);
           const uint32_t st = vp.stage;
@@ -366,6 +380,8 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
         #pragma unroll
         for (int b = 0; b < L::kBufs; ++b)
           if (b < total && ok) qk(b);
+        // Both halves' O have been read before either is written anew.
+        if (kSplit) ok = ok && seq_wait(&bars[L::bJoined], (n & 1) ^ 1, abort_flag, kDevTimeoutMma, 15, (int)n);
         uint32_t flip = 0;
         for (int g = 0; g < total && ok; g += L::kBufs) {
           #pragma unroll
@@ -400,7 +416,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
     // ------------------------------------------------------------------ item finder
     regs_dec<kPrRegsLow>();
     TileList list;
-    const long long total = list.init(p.seq_start, p.n_seq, p.n_tok, 256) * p.q_heads;
+    const long long total = list.init(p.seq_start, p.n_seq, p.n_tok, kRows) * p.q_heads;
     if (blockIdx.x == 0) {  // offsets that decrease or reach outside leave their sequence out: say so
       for (int s = lane; s < p.n_seq; s += 32) {
         const int a = __ldg(p.seq_start + s), b = __ldg(p.seq_start + s + 1);
@@ -417,7 +433,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
         const int s = list.find(x / p.q_heads, &lv);
         int first, len;
         seq_range(p.seq_start, p.n_tok, s, &first, &len);
-        it = make_int4(first + lv * 256, len - lv * 256, lv * 2, (int)(x % p.q_heads));
+        it = make_int4(first + lv * kRows, len - lv * kRows, lv * (kRows / 128), (int)(x % p.q_heads));
       } else if ((long long)r * gridDim.x < total) {
         continue;  // a round that is not full: none for this block
       }
@@ -438,20 +454,23 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
     const int row = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t o_tm = tmem + lane_base + L::kO + half * D;
+    uint32_t joins = 0;
     uint32_t no = 0, tiles_before = 0;  // P V products of this query tile and key tiles of earlier items
     uint32_t ns = 0;                    // bit b: the phase of buffer b's next S for this query tile
     int4 it;
     while (next_item(&it, 42 + half)) {
       const uint32_t ring0 = 2 * tiles_before;  // the item's first place in the ring
-      const int all_tiles = it.z + (it.y > 128 ? 2 : 1);
+      const bool two = !kSplit && it.y > 128;
+      const int all_tiles = it.z + (two ? 2 : 1);
       tiles_before += all_tiles;
-      const bool two = it.y > 128;
       const int nA = it.z + 1;
-      if (half == 1 && !two) continue;  // no tile B
-      const int tiles = it.z + 1 + half;
-      const bool valid = half * 128 + row < it.y;
+      if (!kSplit && half == 1 && !two) continue;  // no tile B
+      const int row0 = kSplit ? 0 : half * 128;                                    // of the item's rows
+      const int tiles = kSplit ? (all_tiles - half + 1) / 2 : it.z + 1 + half;     // key tiles that this half takes
+      const bool valid = row0 + row < it.y;
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < tiles; ++j) {
+      for (int i = 0; i < tiles; ++i) {
+        const int j = kSplit ? 2 * i + half : i;  // the key tile
         const int g = !two ? j : j < nA ? 2 * j + half : 2 * nA;  // the tile's place in the order of S
         const uint32_t buf = g % L::kBufs;
         const uint32_t s_tm = tmem + lane_base + buf * 128;
@@ -461,7 +480,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
         // The exponentials of the first 64 keys are taken with the maximum in use while the true maximum of all 128 is
         // still being found: the comparisons run in the special-function unit's shadow. Only where the
         // maximum has to move are they taken again.
-        const bool diagonal = j == tiles - 1;  // key c is kept by row r iff c <= r
+        const bool diagonal = kSplit ? j == all_tiles - 1 : j == tiles - 1;  // key c is kept by row r iff c <= r
         uint32_t a0[32], a1[32], a2[32], a3[32], w0[16], w1[16];
         tmem_ld32(s_tm, a0);
         tmem_ld32(s_tm + 32, a1);
@@ -516,8 +535,8 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
           const float a = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
           m = m_new;
           l *= a;
-          if (j > 0) {  // once the last P V is done
-            if (!warp_wait(&bars[L::bO + half], (no + j - 1) & 1, abort_flag, kDevTimeoutSoftmax, 22 + half, (int)no, j)) goto done;
+          if (i > 0) {  // once the last P V is done
+            if (!warp_wait(&bars[L::bO + half], (no + i - 1) & 1, abort_flag, kDevTimeoutSoftmax, 22 + half, (int)no, j)) goto done;
             tc_fence_after();
             #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -543,10 +562,10 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
           tmem_wait_st();
           warp_arrive_tc(&bars[L::bP + buf * kPrParts + part]);
         };
-        if (diagonal && it.y < (half + 1) * 128) {  // the tile reaches behind the sequence's end: clear its value rows there
+        if (diagonal && it.y < row0 + 128) {  // the tile reaches behind the sequence's end: clear its value rows there
           const uint32_t v = ring0 + (j == all_tiles - 1 ? 2 * all_tiles - 1 : 2 * j + 2), st = v % L::kStages;
           if (!warp_wait(&bars[L::bFull + st], (v / L::kStages) & 1, abort_flag, kDevTimeoutSoftmax, 26 + half, (int)v, j)) goto done;
-          if (half * 128 + row >= it.y) {
+          if (row0 + row >= it.y) {
             uint8_t* r = smem + L::kRing + st * L::kTileBytes + row * 128;
             #pragma unroll
             for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(r + (c >> 3) * L::kBlock + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -566,29 +585,62 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
       }
       // ---- epilogue
       no += tiles;
-      if (!warp_wait(&bars[L::bO + half], (no - 1) & 1, abort_flag, kDevTimeoutSoftmax, 24 + half, (int)no)) goto done;
+      if (tiles > 0 && !warp_wait(&bars[L::bO + half], (no - 1) & 1, abort_flag, kDevTimeoutSoftmax, 24 + half, (int)no)) goto done;
       tc_fence_after();
-      {
+      const long long tok = (long long)it.x + row0 + row;
+      T* dst = static_cast<T*>(p.o.ptr) + it.w * p.o.sh + tok * p.o.st;
+      const auto store32 = [&](const uint32_t (&ov)[32], float f, int c) {
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t w[4];
+          #pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = E::pack(__uint_as_float(ov[8 * e + 2 * i]) * f, __uint_as_float(ov[8 * e + 2 * i + 1]) * f);
+          reinterpret_cast<uint4*>(dst)[c * 4 + e] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      };
+      if constexpr (!kSplit) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const long long tok = (long long)it.x + half * 128 + row;
-        T* dst = static_cast<T*>(p.o.ptr) + it.w * p.o.sh + tok * p.o.st;
         #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t ov[32];
           tmem_ld32(o_tm + c * 32, ov);
-          tmem_wait_ld();
-          if (valid) {
-            #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
-              #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                w[i] = E::pack(__uint_as_float(ov[8 * e + 2 * i]) * inv, __uint_as_float(ov[8 * e + 2 * i + 1]) * inv);
-              reinterpret_cast<uint4*>(dst)[c * 4 + e] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
+          tmem_wait_ld(ov);
+          if (valid) store32(ov, inv, c);
         }
         if (valid && p.lse) p.lse[(long long)it.w * p.n_tok + tok] = (m + log2f(l)) * 0.69314718055994530942f;
+      } else {
+        float2* ml = reinterpret_cast<float2*>(smem + L::kQ + L::kTileBytes);  // where the second Q tile would be
+        ml[half * 128 + row] = make_float2(m, l);
+        warp_arrive_tc(&bars[L::bJoin]);
+        if (!warp_wait(&bars[L::bJoin], joins & 1, abort_flag, kDevTimeoutSoftmax, 28 + half, (int)joins)) goto done;
+        ++joins;
+        tc_fence_after();
+        const float2 other = ml[(half ^ 1) * 128 + row];
+        const float2 a = half == 0 ? make_float2(m, l) : other, b = half == 0 ? other : make_float2(m, l);
+        const float top = fmaxf(a.x, b.x);
+        float wa = a.x == -INFINITY ? 0.f : ex2_approx(a.x - top), wb = b.x == -INFINITY ? 0.f : ex2_approx(b.x - top);
+        const float sum = fmaf(wa, a.y, wb * b.y);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        wa *= inv;
+        wb *= inv;
+        const bool both = all_tiles > 1;  // else O_B has not been written
+        #pragma unroll
+        for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {  // this half's share of the columns
+          uint32_t ov[32], ob[32];
+          tmem_ld32(tmem + lane_base + L::kO + c * 32, ov);
+          tmem_ld32(tmem + lane_base + L::kO + D + c * 32, ob);
+          tmem_wait_ld(ov);
+          tmem_wait_ld(ob);
+          #pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float x = __uint_as_float(ov[e]) * wa;
+            ov[e] = __float_as_uint(both ? fmaf(__uint_as_float(ob[e]), wb, x) : x);
+          }
+          if (valid) store32(ov, 1.f, c);
+        }
+        if (valid && half == 0 && p.lse) p.lse[(long long)it.w * p.n_tok + tok] = (top + log2f(sum)) * 0.69314718055994530942f;
+        warp_arrive_tc(&bars[L::bJoined]);
       }
       tc_fence_before();  // before the next item's first P: its P V overwrites O
     }
