@@ -12,17 +12,23 @@
 // One (token, pair) angle serves every head, so the double work is a few percent of the pass.
 //
 // An E4M3 cache stores e4m3(x / scale) from the fp32 rotated value: rounding to the input type first
-// would round twice.
+// would round twice. The quotient is taken as x * (1 / scale), 1.5 units in the last place of fp32 off at most.
 //
 // Bound by memory: every 16-byte chunk is read once and written once or twice (keys: packed output
 // and cache). A thread moves 32 bytes of a head: chunks 2i and 2i + 1, or, for paired halves, chunk i
 // of each half, so both elements of each pair are in one thread.
+//
+// A token's place (sequence, position and page) is a chain of three loads, its angles some hundred instructions. The
+// inputs depend on neither: each thread asks for its first 32 bytes before them. A block takes one token. With few tokens it has a
+// thread for each 32 bytes where the heads allow it (16 tokens of 24 and 8 heads: 3.6 us). With many it has 128, so that many
+// blocks of an SM are copying while others wait for their angles: 9177 tokens of 32 and 8 heads take 43 us, 5.6 TB/s; 61 us
+// with 384 threads a token, 45 with two tokens in 128.
 #pragma once
 #include "clear_seq_common.cuh"
 
 namespace clear {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendMaxThreads = 512;
 constexpr int kAppendMaxPairs = 64;
 
 struct SeqAppendParams {
@@ -51,80 +57,81 @@ __device__ __forceinline__ int seq_of_token(const int* __restrict__ seq_start, i
   return (__ldg(seq_start + lo) <= t && t < __ldg(seq_start + lo + 1)) ? lo : -1;
 }
 
-// E: element type; kF8: E4M3 cache; D: head dim; kHalves: pairs of halves; kTok: tokens per block.
-template <typename E, bool kF8, int D, bool kHalves, int kTok>
-__global__ void __launch_bounds__(kAppendThreads) clear_seq_append_kernel(const __grid_constant__ SeqAppendParams p) {
+// E: element type; kF8: E4M3 cache; D: head dim; kHalves: pairs of halves.
+template <typename E, bool kF8, int D, bool kHalves>
+__global__ void __launch_bounds__(kAppendMaxThreads) clear_seq_append_kernel(const __grid_constant__ SeqAppendParams p) {
   using T = typename E::type;
   constexpr int kItems = D / 16;  // 32-byte items per head
-  __shared__ float2 cs[kTok][kAppendMaxPairs];
-  __shared__ int tok_pos[kTok];            // position, or -1: nothing to do
-  __shared__ long long k_row[kTok], v_row[kTok];  // element offset of the cache row, or -1: not stored
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t0 = blockIdx.x * kTok;
+  __shared__ float2 cs[kAppendMaxPairs];  // pair 8 i + e at 8 e + i: threads of neighbouring items read neighbours
+  __shared__ long long row_at[2];         // element offset of the cache row of k and of v, or -1: not stored
+  __shared__ int pos_at;                  // position, or -1: nothing to do
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int t = blockIdx.x;
+  const int items = (p.q_heads + 2 * p.kv_heads) * kItems;
+  const int rot_items = p.rot >> 4;
 
-  if (warp < kTok) {
-    const int t = t0 + warp;
+  // Item i: 32 bytes of a query, key or value head.
+  const auto load = [&](int i, uint4* w0, uint4* w1) {
+    int h = i / kItems;
+    const int it = i % kItems;
+    const SeqView& in = h < p.q_heads ? p.q : h < p.q_heads + p.kv_heads ? p.k : p.v;
+    const bool is_v = h >= p.q_heads + p.kv_heads;
+    h -= h < p.q_heads ? 0 : is_v ? p.q_heads + p.kv_heads : p.q_heads;
+    const bool apart = kHalves && !is_v && it < rot_items;
+    const T* src = static_cast<const T*>(in.ptr) + h * in.sh + t * in.st;
+    *w0 = reinterpret_cast<const uint4*>(src)[apart ? it : 2 * it];  // plain loads: outputs may be the inputs
+    *w1 = reinterpret_cast<const uint4*>(src)[apart ? it + rot_items : 2 * it + 1];
+  };
+  uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+  if (tid < items) load(tid, &w0, &w1);
+
+  if (tid < 32) {
     int pos = -1;
     long long kr = -1, vr = -1;
-    if (t < p.n_tok) {
-      const int s = seq_of_token(p.seq_start, p.n_seq, t, lane);
-      if (s >= 0) {
-        const long long x = (long long)__ldg(p.seq_len + s) - ((long long)__ldg(p.seq_start + s + 1) - t);
-        if (x >= 0) {  // a negative position is padding
-          pos = (int)x;
-          const int pg = p.c.page_div.div(pos);
-          const int row = pos - pg * p.c.page_size;
-          const int id = pg < p.c.max_pages ? __ldg(p.c.table + s * p.c.table_stride + pg) : -1;
-          if ((unsigned)id < (unsigned)p.c.n_pages) {
-            kr = id * p.c.ks[0] + row * p.c.ks[1];
-            vr = id * p.c.vs[0] + row * p.c.vs[1];
-          } else if (lane == 0) {
-            record_bad_index(kSiteAppendPage, s, pos, id);
-          }
+    const int s = seq_of_token(p.seq_start, p.n_seq, t, lane);
+    if (s >= 0) {
+      const long long x = (long long)__ldg(p.seq_len + s) - ((long long)__ldg(p.seq_start + s + 1) - t);
+      if (x >= 0) {  // a negative position is padding
+        pos = (int)x;
+        const int pg = p.c.page_div.div(pos);
+        const int row = pos - pg * p.c.page_size;
+        const int id = pg < p.c.max_pages ? __ldg(p.c.table + s * p.c.table_stride + pg) : -1;
+        if ((unsigned)id < (unsigned)p.c.n_pages) {
+          kr = id * p.c.ks[0] + row * p.c.ks[1];
+          vr = id * p.c.vs[0] + row * p.c.vs[1];
+        } else if (lane == 0) {
+          record_bad_index(kSiteAppendPage, s, pos, id);
         }
       }
     }
     if (lane == 0) {
-      tok_pos[warp] = pos;
-      k_row[warp] = kr;
-      v_row[warp] = vr;
+      pos_at = pos;
+      row_at[0] = kr;
+      row_at[1] = vr;
     }
   }
   __syncthreads();
-  const int pairs = p.rot >> 1;
-  for (int i = threadIdx.x; i < kTok * pairs; i += kAppendThreads) {
-    const int j = i / pairs, pr = i - j * pairs;
-    if (tok_pos[j] >= 0) {
-      const double turn = (double)tok_pos[j] * p.turns[pr];
-      float s, c;
-      sincospif((float)(2.0 * (turn - rint(turn))), &s, &c);
-      cs[j][pr] = make_float2(c, s);
-    }
+  const int pos = pos_at;
+  if (pos < 0) return;
+  for (int i = tid; i < (p.rot >> 1); i += blockDim.x) {
+    const double turn = (double)pos * p.turns[i];
+    float s, c;
+    sincospif((float)(2.0 * (turn - rint(turn))), &s, &c);
+    cs[(i & 7) * 8 + (i >> 3)] = make_float2(c, s);
   }
   __syncthreads();
 
-  const int heads = p.q_heads + 2 * p.kv_heads;
-  const int per_tok = heads * kItems;
-  const int rot_items = p.rot >> 4;
-  for (int i = threadIdx.x; i < kTok * per_tok; i += kAppendThreads) {
-    const int j = kTok == 1 ? 0 : i / per_tok;
-    const int r = i - j * per_tok;
-    if (tok_pos[j] < 0) continue;
-    int h = r / kItems;
-    const int it = r % kItems;
-    const long long t = t0 + j;
+  for (int i = tid; i < items; i += blockDim.x) {
+    if (i != tid) load(i, &w0, &w1);
+    int h = i / kItems;
+    const int it = i % kItems;
     const bool is_q = h < p.q_heads;
-    if (is_q && !p.q.ptr) continue;
     if (!is_q) h -= p.q_heads;
     const bool is_v = !is_q && h >= p.kv_heads;
     if (is_v) h -= p.kv_heads;
-    const SeqView& in = is_q ? p.q : is_v ? p.v : p.k;
     const bool turned = !is_v && it < rot_items;
-    const int c0 = (kHalves && it < rot_items) ? it : 2 * it;
-    const int c1 = (kHalves && it < rot_items) ? it + rot_items : 2 * it + 1;
-    const T* src = static_cast<const T*>(in.ptr) + h * in.sh + t * in.st;
-    const uint4 w0 = reinterpret_cast<const uint4*>(src)[c0];  // plain loads: outputs may be the inputs
-    const uint4 w1 = reinterpret_cast<const uint4*>(src)[c1];
+    const int c0 = (kHalves && turned) ? it : 2 * it;
+    const int c1 = (kHalves && turned) ? it + rot_items : 2 * it + 1;
     uint32_t x[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
     float f[16];
     #pragma unroll
@@ -136,18 +143,18 @@ __global__ void __launch_bounds__(kAppendThreads) clear_seq_append_kernel(const 
       if (kHalves) {
         #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float2 a = cs[j][it * 8 + e];
+          const float2 w = cs[e * 8 + it];
           const float lo = f[e], hi = f[8 + e];
-          f[e] = fmaf(lo, a.x, -hi * a.y);
-          f[8 + e] = fmaf(lo, a.y, hi * a.x);
+          f[e] = fmaf(lo, w.x, -hi * w.y);
+          f[8 + e] = fmaf(lo, w.y, hi * w.x);
         }
       } else {
         #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float2 a = cs[j][it * 8 + e];
+          const float2 w = cs[e * 8 + it];
           const float lo = f[2 * e], hi = f[2 * e + 1];
-          f[2 * e] = fmaf(lo, a.x, -hi * a.y);
-          f[2 * e + 1] = fmaf(lo, a.y, hi * a.x);
+          f[2 * e] = fmaf(lo, w.x, -hi * w.y);
+          f[2 * e + 1] = fmaf(lo, w.y, hi * w.x);
         }
       }
       #pragma unroll
@@ -163,17 +170,16 @@ __global__ void __launch_bounds__(kAppendThreads) clear_seq_append_kernel(const 
       }
     }
     if (!is_q) {
-      const long long row = is_v ? v_row[j] : k_row[j];
+      const long long row = row_at[is_v];
       if (row >= 0) {
         const long long at = row + h * (is_v ? p.c.vs[2] : p.c.ks[2]);
         void* base = is_v ? p.c.v : p.c.k;
         if constexpr (kF8) {
-          const float scale = __ldg((is_v ? p.c.v_scale : p.c.k_scale) + h);
+          const float inv = 1.f / __ldg((is_v ? p.c.v_scale : p.c.k_scale) + h);
           uint32_t y[4];
           #pragma unroll
           for (int e = 0; e < 4; ++e)
-            y[e] = pack_e4m3x2(f[4 * e] / scale, f[4 * e + 1] / scale) |
-                   (pack_e4m3x2(f[4 * e + 2] / scale, f[4 * e + 3] / scale) << 16);
+            y[e] = pack_e4m3x2(f[4 * e] * inv, f[4 * e + 1] * inv) | (pack_e4m3x2(f[4 * e + 2] * inv, f[4 * e + 3] * inv) << 16);
           uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + at);
           dst[c0] = make_uint2(y[0], y[1]);
           dst[c1] = make_uint2(y[2], y[3]);

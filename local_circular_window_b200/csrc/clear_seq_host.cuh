@@ -76,13 +76,13 @@ clear_status_t check_seq_cache(const clear_seq_params_t* p, const clear_seq_cach
 }
 
 // ---------------------------------------------------------------------------------------- append
+constexpr int kAppendMany = 1024;  // tokens from which blocks are small
+
 template <typename E, bool kF8, int D, bool kHalves>
 clear_status_t launch_append(const SeqAppendParams& a, cudaStream_t stream) {
-  // Four tokens a block share the block's set-up; with few tokens one each spreads them over the SMs.
-  if (a.n_tok >= 4096)
-    clear_seq_append_kernel<E, kF8, D, kHalves, 4><<<(a.n_tok + 3) / 4, kAppendThreads, 0, stream>>>(a);
-  else
-    clear_seq_append_kernel<E, kF8, D, kHalves, 1><<<a.n_tok, kAppendThreads, 0, stream>>>(a);
+  const int items = ((a.q_heads + 2 * a.kv_heads) * (D / 16) + 31) & ~31;
+  const int most = a.n_tok >= kAppendMany ? 128 : kAppendMaxThreads;
+  clear_seq_append_kernel<E, kF8, D, kHalves><<<a.n_tok, items < most ? items : most, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? CLEAR_OK : CLEAR_ERR_CUDA;
 }
 
