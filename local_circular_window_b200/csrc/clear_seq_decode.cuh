@@ -483,7 +483,8 @@ __global__ void __launch_bounds__(kDecThreads, kDecPerSm) clear_seq_decode_kerne
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float m_new = fmaxf(m[n][u], top);
+            // A head that does not ask for it keeps its maximum: its result has no part in its neighbours'.
+            const float m_new = top > m[n][u] + kDecRescale || (m[n][u] == -INFINITY && top > m[n][u]) ? top : m[n][u];
             const float a = m[n][u] == -INFINITY ? 0.f : ex2_approx(m[n][u] - m_new);
             m[n][u] = m_new;
             l[n][u] *= a;

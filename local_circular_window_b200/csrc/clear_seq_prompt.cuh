@@ -531,7 +531,8 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
         const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
         const bool grow = top > m + kPrRescale || (m == -INFINITY && top > m);
         if (__any_sync(0xffffffffu, grow)) {
-          const float m_new = fmaxf(m, top);
+          // A row that does not ask for it keeps its maximum: its result has no part in its neighbours'.
+          const float m_new = grow ? top : m;
           const float a = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
           m = m_new;
           l *= a;

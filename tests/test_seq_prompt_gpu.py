@@ -38,6 +38,11 @@ CASES = [  # lens, q_heads, kv_heads, d, dtype
     ([3] * 50 + [300, 0, 0, 2], 2, 2, 64, torch.bfloat16),   # more sequences than lanes
     ([0, 0, 5], 1, 1, 128, torch.float16),
     ([1537], 2, 1, 128, torch.bfloat16),
+    # few long sequences: key tiles split between the two halves of a block
+    ([513], 1, 1, 64, torch.float16),
+    ([600, 1, 1100], 3, 3, 128, torch.bfloat16),
+    ([1025, 0, 640], 2, 1, 64, torch.bfloat16),
+    ([2300], 9, 3, 128, torch.float16),
 ]
 
 
@@ -60,18 +65,19 @@ def test_many_items_for_each_block():
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
-def test_sequences_do_not_touch_each_other():
-    lens = [100, 200, 60]
-    q, k, v, ss = (x.cuda() for x in make(21, lens, 2, 1, 64, torch.bfloat16, behind=90))
+@pytest.mark.parametrize("a,b,c", [(100, 200, 60), (700, 100, 1000)])
+def test_sequences_do_not_touch_each_other(a, b, c):
+    q, k, v, ss = (x.cuda() for x in make(21, [a, b, c], 2, 1, 64, torch.bfloat16, behind=90))
+    n = a + b + c
     o = torch.full_like(q, 7.0)
     lse = torch.full(q.shape[:2], 7.0, device="cuda")
     L.clear_attn_prompt_fwd(q, k, v, ss, o=o, lse=lse)
-    assert (o[:, 360:] == 7).all() and (lse[:, 360:] == 7).all()  # rows behind the last sequence
+    assert (o[:, n:] == 7).all() and (lse[:, n:] == 7).all()  # rows behind the last sequence
     for x in (q, k, v):
-        x[:, 100:300] = math.nan
-        x[:, 360:] = math.inf
+        x[:, a:a + b] = math.nan
+        x[:, n:] = math.inf
     o2, lse2 = L.clear_attn_prompt_fwd(q, k, v, ss)
-    for t in (slice(0, 100), slice(300, 360)):
+    for t in (slice(0, a), slice(a + b, n)):
         assert torch.equal(o2[:, t], o[:, t]) and torch.equal(lse2[:, t], lse[:, t])
 
 
