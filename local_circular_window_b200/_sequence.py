@@ -67,7 +67,7 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 def _view(name, t, shape, dtype, device):
     """The packed view of a [heads, tokens, d] tensor, checked."""
-    if t.shape != shape or t.dtype is not dtype or t.device != device:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device.index:
         _wrong(name, t, shape, dtype, device)
     h, n, e = t.stride()
     if e != 1:
@@ -77,7 +77,7 @@ def _view(name, t, shape, dtype, device):
 
 def _dense(name, t, shape, dtype, device):
     """The address of a contiguous tensor, checked."""
-    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device.index or not t.is_contiguous():
         _wrong(name, t, shape, dtype, device)
     return t.data_ptr()
 
@@ -131,9 +131,9 @@ def _cache(k_pages, v_pages, page_table, k_scale, v_scale, kv_heads, d, dtype, d
         raise ValueError(f"pages must be {dtype} or float8_e4m3fn")
     kp, kr, kh, ke = k_pages.stride()
     vp, vr, vh, ve = v_pages.stride()
-    if ke != 1 or ve != 1 or k_pages.device != device or v_pages.device != device:
+    if ke != 1 or ve != 1 or k_pages.get_device() != device.index or v_pages.get_device() != device.index:
         raise ValueError(f"pages must have contiguous rows and lie on {device}")
-    if page_table.dim() != 2 or page_table.dtype is not torch.int32 or page_table.device != device:
+    if page_table.dim() != 2 or page_table.dtype is not torch.int32 or page_table.get_device() != device.index:
         raise ValueError(f"page_table must be int32 [sequences, pages] on {device}")
     max_pages = page_table.shape[1]
     row, step = page_table.stride()

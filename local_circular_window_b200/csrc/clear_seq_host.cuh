@@ -283,9 +283,12 @@ clear_status_t clear_attn_cache_append(const clear_seq_params_t* params, const c
     if (rope->rot % 16) return CLEAR_ERR_UNSUPPORTED;
     a.rot = rope->rot;
     halves = rope->pairing == CLEAR_PAIR_HALVES;
-    const double base = (double)rope->theta * std::pow((double)rope->ntk, (double)a.rot / (a.rot - 2));
-    for (int i = 0; i < a.rot / 2; ++i)
-      a.turns[i] = std::pow(base, -2.0 * i / a.rot) / 6.283185307179586476925286766559;
+    // Rates base^(-2i / rot) as powers of one ratio, in extended precision: 64 steps lose less than a double's last bit, and
+    // 64 calls of pow would take as long as the launch.
+    const long double base = (long double)rope->theta * std::pow((long double)rope->ntk, (long double)a.rot / (a.rot - 2));
+    const long double ratio = std::pow(base, -2.0L / a.rot);
+    long double turn = 1.0L / 6.283185307179586476925286766559L;
+    for (int i = 0; i < a.rot / 2; ++i, turn *= ratio) a.turns[i] = (double)turn;
   }
   int num_sms = 0;
   if ((st = check_device(&num_sms)) != CLEAR_OK) return st;
