@@ -16,7 +16,7 @@
 // tiles of 64. All units' tiles form one line, and each of the grid's blocks takes an equal piece of it, so
 // ragged batches and single long sequences load every SM alike. A unit's start counts as some tiles more: finishing a
 // piece costs about a microsecond, so a block with many short units has fewer tiles (48 sequences of 128 to
-// 8192 tokens in bf16: 83 us without, 71 us with; 96 of 94 to 6000 in E4M3: 92 and 70 us). A piece that is not a whole unit
+// 8192 tokens in bf16: 83 us without, 71 us with; 96 of 94 to 6000 in E4M3: 92 and 70 us, with two blocks per SM). A piece that is not a whole unit
 // leaves (m, l, O) in the workspace, and a second small kernel joins the pieces of a unit in
 // their order along the keys: no atomics, the same bits on every run. It is launched as a
 // programmatic dependent, so its launch hides behind the first kernel.
@@ -51,9 +51,8 @@ constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kDecSlice = 16;                        // keys a warp takes at a time
 constexpr int kDecTile = kDecWarps * kDecSlice;      // keys of the work split's unit
 constexpr int kDecRows = 16;                         // query heads of one unit
-constexpr int kDecPerSm = 2;                         // resident blocks per SM
 constexpr int kDecMaxStages = 8;
-constexpr int kDecMaxBlocks = kDecPerSm * 160;       // blocks of the grid: as many as are resident at once
+constexpr int kDecMaxBlocks = 3 * 160;               // blocks of the grid: as many as are resident at once
 constexpr float kDecRescale = 8.0f;                  // log2 units a head's maximum may grow before O is rescaled
 
 struct SeqDecodeParams {
@@ -110,8 +109,11 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
 
 template <bool kF8, int D, int kN>
 struct DecLayout {
-  static constexpr int kRing = kN == 1 ? 24576 : 20480;              // bytes of a warp's ring of copies, at most
   static constexpr int kRowBytes = D * (kF8 ? 1 : 2);
+  // Resident blocks per SM. E4M3 slices bring half the bytes for the same instructions and want more warps: 96 sequences of 94 to
+  // 6000 tokens, d = 128, take 71 us with two and 62 us with three. (bf16 at d = 64: 200000 tokens 72 and 79 us.)
+  static constexpr int kPerSm = kF8 && kN == 1 ? 3 : 2;
+  static constexpr int kRing = kPerSm == 3 ? 12288 : kN == 1 ? 24576 : 20480;  // bytes of a warp's ring of copies, at most
   static constexpr int kBox = kRowBytes < 128 ? kRowBytes : 128;     // bytes of row in one box: one swizzled block of 16 rows
   static constexpr int kBoxes = kRowBytes / kBox;
   static constexpr int kSide = kDecSlice * kRowBytes;                // the slice's keys; its values follow
@@ -124,7 +126,7 @@ struct DecLayout {
   static constexpr int kBars = kJoinMl + kDecWarps * kRows * 8;      // a barrier per warp and stage
   static constexpr int kLoc = kBars + kDecWarps * kDecMaxStages * 8; // dec_locate's scratch, then the flag of an expired wait
   static constexpr int kSmem = kLoc + 96;
-  static_assert(kDecPerSm * (kSmem + 1024) <= 233472, "resident blocks (1 KB of each is the system's)");
+  static_assert(kPerSm * (kSmem + 1024) <= 233472, "resident blocks (1 KB of each is the system's)");
   // Byte offset of 16-byte chunk c of row r within a side.
   static __device__ __forceinline__ int at(int r, int c) {
     if constexpr (kBox == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
@@ -204,7 +206,7 @@ __device__ __forceinline__ DecStart dec_locate(const SeqDecodeParams& p, long lo
 
 // kN: tiles of 8 query heads (1 or 2).
 template <typename E, bool kF8, int D, int kN>
-__global__ void __launch_bounds__(kDecThreads, kDecPerSm) clear_seq_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+__global__ void __launch_bounds__(kDecThreads, DecLayout<kF8, D, kN>::kPerSm) clear_seq_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ SeqDecodeParams p) {
   using T = typename E::type;
   using L = DecLayout<kF8, D, kN>;

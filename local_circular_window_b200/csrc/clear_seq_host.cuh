@@ -137,7 +137,8 @@ clear_status_t launch_decode(SeqDecodeParams p, int num_sms, cudaStream_t stream
   const int smem = p.group <= 8 ? L1::kSmem : L2::kSmem;
   static std::atomic<unsigned long long> done[2];
   if (!allow_smem(reinterpret_cast<const void*>(kernel), smem, &done[p.group <= 8 ? 0 : 1])) return CLEAR_ERR_CUDA;
-  const int blocks = kDecPerSm * num_sms < kDecMaxBlocks ? kDecPerSm * num_sms : kDecMaxBlocks;
+  const int resident = (p.group <= 8 ? L1::kPerSm : L2::kPerSm) * num_sms;
+  const int blocks = resident < kDecMaxBlocks ? resident : kDecMaxBlocks;
   kernel<<<blocks, kDecThreads, smem, stream>>>(mk, mv, p);
   if (cudaGetLastError() != cudaSuccess) return CLEAR_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
