@@ -369,8 +369,9 @@ CLEAR_API clear_status_t clear_attn_bwd(const clear_attn_params_t* params, const
  * memory) or CLEAR_ERR_CUDA (the stream reported a CUDA error). */
 CLEAR_API clear_status_t clear_attn_check(void* stream);
 
-/* Context of the expired wait behind the last CLEAR_ERR_DEVICE_TIMEOUT that clear_attn_check()
- * returned on this host thread (zeros if none): {code (1 producer, 3 MMA, 4 softmax), wait site,
+/* Context of the expired wait or bad index behind the last CLEAR_ERR_DEVICE_TIMEOUT or
+ * CLEAR_ERR_DEVICE_INDEX that clear_attn_check() returned on this host thread (zeros if none):
+ * {code (1 producer, 3 MMA, 4 softmax, 16 an index out of range), site,
  * CTA index, thread index, phase parity (-1 for a polling loop), three site-specific counters}.
  * For diagnosis only; the layout may change between versions. */
 CLEAR_API void clear_attn_device_diag(int* out8);

@@ -24,9 +24,9 @@
 // Inside a block each of 4 warps takes every fourth 16-key slice and runs alone: its own ring of
 // copies, its own running (m, l, O); the four are joined once per piece. The copies run on into the block's next
 // piece while this one is finished: a batch of many short sequences streams like one long one. Where pages hold a multiple of 16
-// rows, a slice lies in one page and TMA brings it (one box per 128 bytes of row: two to four instructions a
-// slice, by one lane, against some 250 when every lane copies a row of its own: bulk copies take uniform operands,
-// so 32 addresses are a loop). Other page sizes take 16-byte asynchronous copies from wherever each row lies.
+// rows, a slice lies in one page and TMA brings it: two instructions by one lane, one box of 16 whole rows each for the keys and the
+// values. (A bulk copy per row by every lane cost some 250 instructions a slice: they take uniform operands, so 32 addresses
+// are a loop.) Other page sizes take 16-byte asynchronous copies from wherever each row lies.
 // Both leave the 128-byte (64-byte) swizzle that keeps ldmatrix free of bank conflicts. Value rows past
 // the sequence's end are cleared before use, so what a page holds behind the last token
 // (NaN included) does not count. Softmax statistics and sums are fp32; probabilities are rounded
