@@ -405,9 +405,9 @@ CLEAR_API clear_status_t clear_attn_selftest_expiry(int limit_ms, void* stream);
  *
  * seq_start (int32 [n_seq + 1]), seq_len (int32 [n_seq]) and the page table are device memory, read
  * when the kernels run: a captured graph may be replayed with other contents. The kernels check them. A
- * sequence whose offsets decrease or leave [0, n_tok], or a page number outside [0, n_pages) or past
- * max_pages, is skipped (a skipped page reads as zeros) and clear_attn_check() reports
- * CLEAR_ERR_DEVICE_INDEX. Tokens behind the last sequence are neither read nor written.
+ * sequence whose offsets decrease or leave [0, n_tok] is skipped, one longer than max_pages pages is cut,
+ * a page number outside [0, n_pages) reads as zeros and is not written, and clear_attn_check() reports
+ * CLEAR_ERR_DEVICE_INDEX. Tokens behind the last sequence do not count and are not written.
  *
  * Statuses: CLEAR_ERR_INVALID_ARG for null or misaligned (16 bytes) pointers, sizes out of range
  * (n_seq in [1, 2^20], n_tok in [1, 2^30]), q_heads not a multiple of kv_heads;
@@ -513,6 +513,7 @@ CLEAR_API size_t clear_attn_prompt_bwd_workspace_size(const clear_seq_params_t* 
  * Gradients are written once, in a fixed order of sums: the same call gives the same bits. Rows behind
  * the last sequence are left as they are. As in the forward, sequences do not touch each other, and a
  * NaN within one sequence may reach rows of its own 128-token block before it.
+ * In fp16, P (dO V^T - D) is rounded to fp16 between the products and must stay within its range.
  */
 CLEAR_API clear_status_t clear_attn_prompt_bwd(const clear_seq_params_t* params, const int* seq_start,
                                                const clear_seq_view_t* q, const clear_seq_view_t* k,

@@ -61,6 +61,7 @@ struct SeqDecodeParams {
   SeqCache c;
   const int* seq_len;
   int n_seq, q_heads, kv_heads, group, m_tiles;
+  int max_len;       // rows that the page table has entries for: longer sequences are cut (and reported)
   float scale_log2;  // log2(e) / sqrt(d)
   int tma;           // pages hold a multiple of 16 rows: slices come by TMA
   // Workspace: per block two pieces (its first and its last): (m, l) and O of 16 rows; and, per
@@ -148,8 +149,12 @@ struct DecStart {
   int seq;
 };
 
-__device__ __forceinline__ int dec_tiles(const SeqDecodeParams& p, int s) {
+__device__ __forceinline__ int dec_len(const SeqDecodeParams& p, int s) {
   const int n = __ldg(p.seq_len + s);
+  return n < p.max_len ? n : p.max_len;
+}
+__device__ __forceinline__ int dec_tiles(const SeqDecodeParams& p, int s) {
+  const int n = dec_len(p, s);
   return n > 0 ? (n - 1) / kDecTile + 1 : 0;
 }
 
@@ -226,7 +231,9 @@ __global__ void __launch_bounds__(kDecThreads, DecLayout<kF8, D, kN>::kPerSm) cl
 
   // Sequences without a key.
   for (int s = blockIdx.x; s < p.n_seq; s += gridDim.x) {
-    if (__ldg(p.seq_len + s) > 0) continue;
+    const int n = __ldg(p.seq_len + s);
+    if (n > p.max_len && tid == 0) record_bad_index(kSiteSeqLen, s, n, p.max_len);
+    if (n > 0) continue;
     for (int i = tid; i < p.q_heads * (D / 8); i += kDecThreads) {
       const int h = i / (D / 8), c = i % (D / 8);
       reinterpret_cast<uint4*>(static_cast<T*>(p.o.ptr) + h * p.o.sh + s * p.o.st)[c] = make_uint4(0, 0, 0, 0);
@@ -270,7 +277,7 @@ __global__ void __launch_bounds__(kDecThreads, DecLayout<kF8, D, kN>::kPerSm) cl
     }
     c.seq = walk_seq;
     c.nt = n - kCost;
-    c.len = __ldg(p.seq_len + c.seq);
+    c.len = dec_len(p, c.seq);
     c.unit = (int)((x - walk_before) / n);
     c.hk = c.unit / p.m_tiles;
     c.mt = c.unit - c.hk * p.m_tiles;

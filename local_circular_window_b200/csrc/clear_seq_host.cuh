@@ -333,6 +333,8 @@ clear_status_t clear_attn_decode(const clear_seq_params_t* params, const clear_s
   p.kv_heads = params->kv_heads;
   p.group = params->q_heads / params->kv_heads;
   p.m_tiles = (p.group + kDecRows - 1) / kDecRows;
+  const long long rows = (long long)cache->max_pages * cache->page_size;
+  p.max_len = rows < INT_MAX ? (int)rows : INT_MAX;
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)params->d));
   char* ws = static_cast<char*>(workspace);
   p.part_o = reinterpret_cast<float*>(ws);

@@ -74,7 +74,9 @@ struct TileList {
   const int* seq_start;
   int n_seq, n_tok, rows;  // rows: query rows of a tile
   int level;               // the level of the last tile asked for
+  int here;                // tiles of that level
   long long above;         // tiles of higher levels
+  int s0, passed;          // sequences before s0 have `passed` tiles of that level, all before the last one asked for
   __device__ __forceinline__ int tiles_of(int s) const {
     int a, n;
     seq_range(seq_start, n_tok, s, &a, &n);
@@ -100,27 +102,29 @@ struct TileList {
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     level = __reduce_max_sync(0xffffffffu, top) - 1;
     above = 0;
+    here = at_level(level);
+    s0 = passed = 0;
     return sum;
   }
-  // Tile y (not before the last one asked for): its sequence and level.
+  // Tile y (not before the last one asked for): its sequence and level. Each level's sequences are gone through once.
   __device__ __forceinline__ int find(long long y, int* lv) {
-    int n = at_level(level);
-    while (y >= above + n && level > 0) {
-      above += n;
+    while (y >= above + here && level > 0) {
+      above += here;
       --level;
-      n = at_level(level);
+      here = at_level(level);
+      s0 = passed = 0;
     }
     *lv = level;
-    int rank = (int)(y - above);  // the rank-th sequence with a tile of this level
-    for (int s0 = 0; s0 < n_seq; s0 += 32) {
+    for (; s0 < n_seq; s0 += 32) {
       const int s = s0 + (threadIdx.x & 31);
       unsigned has = __ballot_sync(0xffffffffu, s < n_seq && tiles_of(s) > level);
       const int c = __popc(has);
+      int rank = (int)(y - above) - passed;
       if (rank < c) {
         while (rank-- > 0) has &= has - 1;
         return s0 + __ffs(has) - 1;
       }
-      rank -= c;
+      passed += c;
     }
     return 0;
   }

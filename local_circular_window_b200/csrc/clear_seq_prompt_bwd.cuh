@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kStatsThreads) clear_seq_bwd_stats_kernel(cons
   const long long t = row / p.q_heads;
   const int h = (int)(row - t * p.q_heads);
   int end = __ldg(p.seq_start + p.n_seq);
-  end = end < p.n_tok ? end : p.n_tok;
+  end = end >= 0 && end < p.n_tok ? end : p.n_tok;
   const bool in = t < end;
   float sum = 0.f;
   if (in) {

@@ -143,8 +143,42 @@ def test_bad_pages_are_reported():
     o, _ = call(q, kp, vp, table, None, lens)
     assert L.clear_attn_check() == 6 and L.clear_attn_check() == 0
     assert torch.equal(o[:, 1], good[:, 1])
-    call(q, kp, vp, table, None, [0, 16 * table.shape[1] + 1])
-    assert L.clear_attn_check() == 6
+    # longer than the table: cut to it, whatever the length says
+    table[0, 1] = table[0, 0]
+    table[1] = table[0]
+    want, _ = call(q, kp, vp, table, None, [0, 16 * table.shape[1]])
+    for n in (16 * table.shape[1] + 1, 2 ** 31 - 1):
+        o, _ = call(q, kp, vp, table, None, [0, n])
+        assert L.clear_attn_check() == 6 and torch.equal(o, want)
+    call(q, kp, vp, table, None, [-5, -2 ** 31])
+    assert L.clear_attn_check() == 0
+
+
+def test_many_sequences_and_heads():
+    gen = torch.Generator().manual_seed(12)
+    lens = torch.randint(0, 40, (1500,), generator=gen).tolist()
+    a = make(13, lens, 2, 1, 64, 16, torch.bfloat16)
+    o, lse = call(*a, lens)
+    q, kp, vp, table, _ = a
+    some = [0, 3, 700, 1498, 1499]
+    verify(o.cpu()[:, some], lse.cpu()[:, some], q[:, some], kp, vp, table[some], None, [lens[i] for i in some])
+    assert not o.isnan().any()
+
+
+def test_two_calls_at_once():
+    # Two streams, a workspace each: neither sees the other.
+    cases = [make(30 + i, [3000, 500], 8, 2, 128, 16, torch.bfloat16) for i in range(2)]
+    want = [call(*c, [3000, 500]) for c in cases]
+    args = [[x.cuda() for x in c[:4]] + [torch.tensor([3000, 500], dtype=torch.int32).cuda()] for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            got[i] = L.clear_attn_decode(*args[i], stream=s)
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert torch.equal(w[0], g[0]) and torch.equal(w[1], g[1])
 
 
 def test_captured_graph_follows_lengths_and_graphs_share_no_state():

@@ -128,3 +128,20 @@ def test_captured_graph_follows_offsets_on_another_stream():
     s.synchronize()
     g.replay()
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_thousands_of_sequences():
+    gen = torch.Generator().manual_seed(40)
+    lens = torch.randint(0, 5, (3000,), generator=gen).tolist()
+    lens[1234], lens[2999] = 400, 150
+    q, k, v, ss = make(41, lens, 2, 1, 64, torch.bfloat16)
+    o, lse = L.clear_attn_prompt_fwd(q.cuda(), k.cuda(), v.cuda(), ss.cuda())
+    some = [0, 1, 7, 500, 1234, 1235, 2500, 2998, 2999]
+    for s in some:
+        t = slice(int(ss[s]), int(ss[s + 1]))
+        n = lens[s]
+        if n:
+            keep = torch.ones(n, n, dtype=torch.bool).tril()
+            for h in range(2):
+                U.check_attention(f"sequence {s}", o.cpu()[h, t], lse.cpu()[h, t], q[h, t], k[0, t], v[0, t], q.dtype, q.dtype, keep)
+    assert not o.isnan().any()
