@@ -381,9 +381,12 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
           }
         };
         ok = seq_wait(&bars[L::bQFull], n & 1, abort_flag, kDevTimeoutMma, 10, (int)n);
+        // S of tile g is issued behind the P V of tile g - kBufs; of g - 1 where one query tile has two buffers for itself, so that
+        // with two buffers S always tells that its query tile's last P V is done.
+        const bool alone = L::kBufs == 2 && !kSplit && !two;
         #pragma unroll
         for (int b = 0; b < L::kBufs; ++b)
-          if (b < total && ok) qk(b);
+          if (b < total && ok && !(alone && b > 0)) qk(b);
         // Both halves' O have been read before either is written anew.
         if (kSplit) ok = ok && seq_wait(&bars[L::bJoined], (n & 1) ^ 1, abort_flag, kDevTimeoutMma, 15, (int)n);
         uint32_t flip = 0;
@@ -392,7 +395,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
           for (int b = 0; b < L::kBufs; ++b) {
             if (g + b < total && ok) {
               pv(b, ((uses >> b) & 1) ^ flip);
-              if (ok && gq < total) qk(b);
+              if (ok && gq < total) qk(alone ? b ^ 1 : b);
             }
           }
           flip ^= 1;
@@ -584,6 +587,10 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
         tmem_st16(s_tm + 64, w0);
         probabilities(a3, base, w1);
         tmem_st16(s_tm + 96, w1);
+        // A wait by parity must be neither two phases ahead of its barrier nor one behind it. With three buffers this tile's S does not
+        // tell that the last tile's P V is done, so that is seen here, while the next one cannot be done.
+        if (L::kBufs == 3 && i > 0 && !warp_wait(&bars[L::bO + half], (no + i - 1) & 1, abort_flag, kDevTimeoutSoftmax, 30 + half, (int)no, j))
+          goto done;
         hand_over(1);
         sum[0] = f32x2_add(sum[0], sum[1]);
         l += f32x2_lo(sum[0]) + f32x2_hi(sum[0]);

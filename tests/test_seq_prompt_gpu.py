@@ -81,14 +81,20 @@ def test_sequences_do_not_touch_each_other(a, b, c):
         assert torch.equal(o2[:, t], o[:, t]) and torch.equal(lse2[:, t], lse[:, t])
 
 
-def test_growing_scores_and_ties():
-    # Keys that grow along the sequence move the running maximum again and again; equal keys tie everywhere.
-    n = 600
-    q, k, v, ss = make(22, [n, n], 2, 1, 64, torch.bfloat16)
-    k[0, :n] = (torch.linspace(-3, 3, n)[:, None] * torch.sign(q[0, :n].float())).to(torch.bfloat16)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [[600, 600], [612, 3, 3, 380]])
+def test_growing_scores_and_ties(lens, d):
+    # Keys that grow along the sequence move the running maximum again and again; equal keys tie everywhere. The second
+    # batch's last query tiles stand alone in their items.
+    q, k, v, ss = make(22, lens, 2, 1, d, torch.bfloat16)
+    n = lens[0]
+    # sum |q k| / sqrt(d) is about 0.8 sqrt(d) |k|, 20 at most
+    k[0, :n] = (torch.linspace(-1, 1, n)[:, None] * (24 / d ** 0.5) * torch.sign(q[0, :n].float())).to(torch.bfloat16)
     k[0, n:] = k[0, n]
     o, lse = L.clear_attn_prompt_fwd(q.cuda(), k.cuda(), v.cuda(), ss.cuda())
-    verify(o.cpu(), lse.cpu(), q, k, v, [n, n])
+    verify(o.cpu(), lse.cpu(), q, k, v, lens)
+    o2, lse2 = L.clear_attn_prompt_fwd(q.cuda(), k.cuda(), v.cuda(), ss.cuda())
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
 def test_strided_views_give_the_same_bits():
