@@ -14,8 +14,6 @@
 
 namespace clear {
 
-enum SeqDtype : int { kSeqBf16 = 0, kSeqFp16 = 1, kSeqE4m3 = 2 };
-
 // Sites of recorded bad indexes (second word of the diagnosis record).
 enum SeqSite : int { kSiteAppendPage = 32, kSiteDecodePage = 33, kSiteSeqStart = 34, kSiteSeqLen = 35 };
 
