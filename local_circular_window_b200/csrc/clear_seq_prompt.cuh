@@ -16,7 +16,7 @@
 // TMEM: two buffers of S (three at d = 64) of 128 columns, then O of A and of B. P overwrites S, 16-bit, two values a
 // column: the 32 keys of each 32 columns go into the first 16. The tiles of S take the buffers in turn, in the order A0, B0,
 // A1, B1, ... (A0, A1, ... for an item without tile B); the next one's product is issued behind the P V that
-// frees its buffer.
+// frees its buffer (clear_seq_order.h, with the waits that follow from it).
 // While one tile's softmax runs, the other tile's products do: the issuer alternates A, B. (An issuer for each
 // tile mixes the two tiles' products in the tensor pipe: 1782 us in place of 1416 at 16896 tokens and 24 heads.)
 //
@@ -41,6 +41,7 @@
 
 #include "clear_common.cuh"
 #include "clear_seq_common.cuh"
+#include "clear_seq_order.h"
 
 namespace clear {
 
@@ -236,6 +237,12 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  const auto order_of = [](const int4& it) {
+    const int tiles = it.z + 1;  // of tile A
+    return kSplit ? PromptOrder<L::kBufs, kSplit>{(tiles + 1) / 2, tiles / 2}
+                  : PromptOrder<L::kBufs, kSplit>{tiles, it.y > 128 ? tiles + 1 : 0};
+  };
+
   // The next item; false at the end of the list (or on an expired wait). Whole warp.
   uint32_t n_item = 0;
   const auto next_item = [&](int4* it, int site) -> bool {
@@ -317,6 +324,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
       const bool two = !kSplit && it.y > 128;
       const int nA = it.z + 1, nB = two ? it.z + 2 : 0;
       const int tiles = two ? nB : nA, total = nA + nB;
+      const PromptOrder<L::kBufs, kSplit> order = order_of(it);
       if (elect_one()) {
         // The next tile of S to be computed (key tile jq of query tile hq), and of P to be used. Ring order:
         // K0, K1, V0, K2, V1, ..., V(tiles-1).
@@ -381,12 +389,10 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
           }
         };
         ok = seq_wait(&bars[L::bQFull], n & 1, abort_flag, kDevTimeoutMma, 10, (int)n);
-        // S of tile g is issued behind the P V of tile g - kBufs; of g - 1 where one query tile has two buffers for itself, so that
-        // with two buffers S always tells that its query tile's last P V is done.
-        const bool alone = L::kBufs == 2 && !kSplit && !two;
+        const bool alone = order.alone();
         #pragma unroll
         for (int b = 0; b < L::kBufs; ++b)
-          if (b < total && ok && !(alone && b > 0)) qk(b);
+          if (b < total && ok && order.first(b)) qk(b);
         // Both halves' O have been read before either is written anew.
         if (kSplit) ok = ok && seq_wait(&bars[L::bJoined], (n & 1) ^ 1, abort_flag, kDevTimeoutMma, 15, (int)n);
         uint32_t flip = 0;
@@ -470,7 +476,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
       const bool two = !kSplit && it.y > 128;
       const int all_tiles = it.z + (two ? 2 : 1);
       tiles_before += all_tiles;
-      const int nA = it.z + 1;
+      const PromptOrder<L::kBufs, kSplit> order = order_of(it);
       if (!kSplit && half == 1 && !two) continue;  // no tile B
       const int row0 = kSplit ? 0 : half * 128;                                    // of the item's rows
       const int tiles = kSplit ? (all_tiles - half + 1) / 2 : it.z + 1 + half;     // key tiles that this half takes
@@ -478,7 +484,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < tiles; ++i) {
         const int j = kSplit ? 2 * i + half : i;  // the key tile
-        const int g = !two ? j : j < nA ? 2 * j + half : 2 * nA;  // the tile's place in the order of S
+        const int g = order.place(half, i);
         const uint32_t buf = g % L::kBufs;
         const uint32_t s_tm = tmem + lane_base + buf * 128;
         if (!warp_wait(&bars[L::bS + 2 * buf + half], (ns >> buf) & 1, abort_flag, kDevTimeoutSoftmax, 20 + half, g, j)) goto done;
@@ -587,9 +593,8 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
         tmem_st16(s_tm + 64, w0);
         probabilities(a3, base, w1);
         tmem_st16(s_tm + 96, w1);
-        // A wait by parity must be neither two phases ahead of its barrier nor one behind it. With three buffers this tile's S does not
-        // tell that the last tile's P V is done, so that is seen here, while the next one cannot be done.
-        if (L::kBufs == 3 && i > 0 && !warp_wait(&bars[L::bO + half], (no + i - 1) & 1, abort_flag, kDevTimeoutSoftmax, 30 + half, (int)no, j))
+        if (order.looks_back(half, i) &&
+            !warp_wait(&bars[L::bO + half], (no + i - 1) & 1, abort_flag, kDevTimeoutSoftmax, 30 + half, (int)no, j))
           goto done;
         hand_over(1);
         sum[0] = f32x2_add(sum[0], sum[1]);

@@ -1,0 +1,53 @@
+"""The prompt kernels where blocks walk several items with d = 128, two buffers of scores and short rings: what one item
+leaves behind for the next, against the definition in 64 bits."""
+import pytest
+import torch
+
+import local_circular_window_b200 as L
+import seq_util as U
+from test_seq_prompt_gpu import make, verify
+
+pytestmark = pytest.mark.gpu
+
+LENS = [260, 1000, 5, 900, 130, 512, 640, 77]  # under 512 tokens a sequence: items are whole
+
+
+def forward(q, k, v, ss):
+    a = [x.cuda() for x in (q, k, v, ss)]
+    o, lse = L.clear_attn_prompt_fwd(*a)
+    assert L.clear_attn_check() == 0
+    for _ in range(3):
+        again = L.clear_attn_prompt_fwd(*a)
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    return o.cpu(), lse.cpu()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_whole_items(dtype):
+    # 864 items with one query tile and with two, about six a block.
+    q, k, v, ss = make(50, LENS, 48, 16, 128, dtype)
+    o, lse = forward(q, k, v, ss)
+    verify(o, lse, q, k, v, LENS, heads=[0, 1, 17, 46, 47])
+
+
+@pytest.mark.parametrize("group", range(4))
+def test_one_warp_moves_its_maximum_late(group):
+    # 32 rows of the second item's tile B (rows 384 to 499) meet their largest scores in the key tile before the diagonal's:
+    # their warp rescales there, the three others do not.
+    lens, d = [500] * 40, 128
+    q, k, v, ss = make(51, lens, 8, 2, d, torch.bfloat16)
+    u = torch.ones(d) / d ** 0.5
+    flat = lambda x: x.float() - (x.float() @ u)[..., None] * u  # noqa: E731
+    q, k = flat(q), flat(k)
+    for s in range(len(lens)):
+        at = 500 * s
+        k[:, at + 256:at + 384] += 10 * u
+        q[:, at + 384 + 32 * group:at + min(500, 416 + 32 * group)] += 12 * u  # 10 * 12 / sqrt(128) = 10.6: 15 powers of two
+    q, k = (x.to(torch.bfloat16) for x in (q, k))
+    o, lse = forward(q, k, v, ss)
+    # sum |q k| / sqrt(d) is about 19 there, and 130 * 2^-24 of it is 1.5e-4: less than SCORE / 2.
+    for s in (0, 7, 39):
+        t = slice(500 * s, 500 * s + 500)
+        keep = torch.ones(500, 500, dtype=torch.bool).tril()
+        for h in (0, 3, 5):
+            U.check_attention(f"sequence {s} head {h}", o[h, t], lse[h, t], q[h, t], k[h // 4, t], v[h // 4, t], q.dtype, q.dtype, keep)

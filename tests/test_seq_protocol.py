@@ -1,0 +1,194 @@
+"""The barriers of the causal prompt forward, gone through on the CPU.
+
+A model of one block: the issuing thread, a tensor pipe that completes products in the order of issue, and the two softmax
+warpgroups as warps of their own, with barriers that are waited for by parity as the hardware's are (a wait passes when the
+barrier's current phase has the other parity, be it one phase further or one phase behind). The order of the
+products and the waits that follow from it are the kernel's own, from csrc/clear_seq_order.h. Random
+schedules, with agents that stall for long, look for a wait that passes before its phase is complete, for an
+accumulator that is read before its last product.
+"""
+import ctypes
+import os
+import random
+import shutil
+import subprocess
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "local_circular_window_b200", "csrc")
+WARPS = 2  # of each warpgroup: enough for a fast one and a slow one
+
+SOURCE = """
+#include "clear_seq_order.h"
+template <int B, bool S> struct X { static int f(int what, int nA, int nB, int x, int y) {
+  const clear::PromptOrder<B, S> o{nA, nB};
+  return what == 0 ? o.place(x, y) : what == 1 ? o.alone() : what == 2 ? o.first(x) : o.looks_back(x, y);
+} };
+extern "C" int order(int bufs, int split, int what, int nA, int nB, int x, int y) {
+  return bufs == 2 ? (split ? X<2, true>::f(what, nA, nB, x, y) : X<2, false>::f(what, nA, nB, x, y))
+                   : (split ? X<3, true>::f(what, nA, nB, x, y) : X<3, false>::f(what, nA, nB, x, y));
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def order(tmp_path_factory):
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("needs g++")
+    at = tmp_path_factory.mktemp("order")
+    (at / "order.cpp").write_text(SOURCE)
+    subprocess.run([gxx, "-std=c++17", "-O1", "-shared", "-fPIC", "-I", CSRC, "-o", str(at / "order.so"), str(at / "order.cpp")], check=True)
+    return ctypes.CDLL(str(at / "order.so")).order
+
+
+class Fault(Exception):
+    pass
+
+
+class Bar:
+    def __init__(self, count):
+        self.count, self.pending, self.phase = count, count, 0
+
+    def arrive(self):
+        self.pending -= 1
+        if self.pending == 0:
+            self.pending, self.phase = self.count, self.phase + 1
+
+
+class Block:
+    """items: for each its number of key tiles and whether it has a tile B."""
+
+    def __init__(self, order, bufs, split, items, rng):
+        self.bufs, self.split, self.items, self.rng = bufs, split, items, rng
+        self.order = lambda what, it, x=0, y=0: order(bufs, int(split), what, *self.counts(it), x, y)
+        self.s = {(b, h): Bar(1) for b in range(bufs) for h in (0, 1)}
+        self.p = {(b, i): Bar(WARPS) for b in range(bufs) for i in (0, 1)}
+        self.o = [Bar(1), Bar(1)]
+        self.join, self.joined = Bar(2 * WARPS), Bar(2 * WARPS)
+        self.pipe = []
+        self.acc = [[], []]   # key tiles whose P V has been added to each accumulator, (item, tile)
+
+    def counts(self, it):
+        tiles, two = it
+        return ((tiles + 1) // 2, tiles // 2) if self.split else (tiles, tiles + 1 if two else 0)
+
+    def wait(self, name, bar, n):
+        """Waits for the end of the barrier's phase number n (from 0), by parity."""
+        while bar.phase & 1 == n & 1:
+            yield
+        if bar.phase < n + 1:
+            raise Fault(f"{name}: a wait for phase {n} passed in phase {bar.phase}")
+
+    def issuer(self):
+        uses = [0] * self.bufs
+        for n, it in enumerate(self.items):
+            nA, nB = self.counts(it)
+            places = {self.order(0, it, h, i): (h, i) for h, m in ((0, nA), (1, nB)) for i in range(m)}
+            total = nA + nB
+            assert sorted(places) == list(range(total))
+            alone = self.order(1, it)
+            ahead = 0
+
+            def issue(b):
+                nonlocal ahead
+                h, _ = places[ahead]
+                assert b == ahead % self.bufs
+                self.pipe.append(("S", self.s[b, h]))
+                ahead += 1
+
+            while ahead < total and self.order(2, it, ahead):
+                issue(ahead % self.bufs)
+            if self.split:
+                yield from self.wait("accumulators", self.joined, n - 1)
+            for g in range(total):
+                h, i = places[g]
+                for part in (0, 1):
+                    yield from self.wait(f"P {part}", self.p[g % self.bufs, part], uses[g % self.bufs])
+                uses[g % self.bufs] += 1
+                self.pipe.append(("PV", self.o[h], h, (n, i)))
+                if ahead < total:
+                    issue((g + 1) % self.bufs if alone else g % self.bufs)
+                yield
+
+    def tensor(self):
+        while True:
+            if self.pipe:
+                op = self.pipe.pop(0)
+                if op[0] == "PV":
+                    self.acc[op[2]].append(op[3])
+                op[1].arrive()
+            yield
+
+    def warp(self, half, w, left):
+        no = joins = 0
+        seen = [0] * self.bufs
+        for n, it in enumerate(self.items):
+            m = self.counts(it)[half]
+            if m == 0 and not self.split:
+                continue
+            for i in range(m):
+                b = self.order(0, it, half, i) % self.bufs
+                yield from self.wait(f"S {half}", self.s[b, half], seen[b])
+                seen[b] += 1
+                yield
+                if i > 0 and self.rng.random() < 0.3:  # the maximum moves: the accumulator is rescaled
+                    yield from self.wait(f"P V {half}, rescaling", self.o[half], no + i - 1)
+                self.p[b, 0].arrive()
+                yield
+                if self.order(3, it, half, i):
+                    yield from self.wait(f"P V {half}, looking back", self.o[half], no + i - 1)
+                self.p[b, 1].arrive()
+                yield
+            no += m
+            if m > 0:
+                yield from self.wait(f"P V {half}, last", self.o[half], no - 1)
+            if not self.split:
+                if self.acc[half][-1] != (n, m - 1):
+                    raise Fault(f"the accumulator of {half} is read at {self.acc[half][-1]} and not {(n, m - 1)}")
+                yield
+                continue
+            self.join.arrive()
+            yield from self.wait("join", self.join, joins)
+            yield
+            joins += 1
+            for h in (0, 1):
+                k = self.counts(it)[h]
+                if k and self.acc[h][-1] != (n, k - 1):
+                    raise Fault(f"the accumulator of {h} is read at {self.acc[h][-1]} and not {(n, k - 1)}")
+            yield
+            self.joined.arrive()
+        left.remove((half, w))
+
+    def run(self):
+        left = {(h, w) for h in (0, 1) for w in range(WARPS)}
+        agents = {("issuer", 0): self.issuer(), ("tensor", 0): self.tensor()}
+        agents |= {x: self.warp(*x, left) for x in left}
+        names, stalled = list(agents), {}
+        rng, idle = self.rng, 0
+        while left:
+            idle += 1
+            assert idle < 100000, "no progress"
+            a = names[int(rng.random() * len(names))]
+            if stalled.get(a, 0) > 0:
+                stalled[a] -= 1
+                continue
+            if rng.random() < 0.04:
+                stalled[a] = int(rng.random() * 60)
+            if a in agents and next(agents[a], "end") == "end":
+                del agents[a]
+
+
+SHAPES = [[(1, True), (2, True), (4, True)], [(3, False), (1, False), (2, False)], [(3, True), (2, False), (1, True), (1, False)],
+          [(5, False), (1, False), (1, False), (2, False)], [(6, True), (1, True), (1, True)]]
+
+
+@pytest.mark.parametrize("bufs", [2, 3])
+@pytest.mark.parametrize("split", [False, True], ids=["whole", "split"])
+def test_every_wait_sees_its_phase(order, bufs, split):
+    rng = random.Random(bufs * 2 + split)
+    for k in range(600):
+        items = rng.choice(SHAPES)
+        if split:
+            items = [(n, False) for n, _ in items]
+        Block(order, bufs, split, items, rng).run()
