@@ -36,6 +36,10 @@ struct PromptOrder {
   CLEAR_ORDER_HD bool looks_back(int half, int i) const {
     return kBufs == 3 ? i > 0 : !kSplit && nB > 0 && half == 1 && i == nA;
   }
+  // Which copy of the halves' exchanged (m, l) an item uses, `joins` items with an exchange lying before it. A half without a key
+  // tile waits for nothing between two items, so it may write while the other half still reads the last item's
+  // sums. It is held at the next exchange's barrier, though: with two copies the one it writes has been read.
+  CLEAR_ORDER_HD int sums(unsigned joins) const { return (int)(joins & 1u); }
 };
 
 }  // namespace clear

@@ -627,7 +627,8 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
         }
         if (valid && p.lse) p.lse[(long long)it.w * p.n_tok + tok] = (m + log2f(l)) * 0.69314718055994530942f;
       } else {
-        float2* ml = reinterpret_cast<float2*>(smem + L::kQ + L::kTileBytes);  // where the second Q tile would be
+        static_assert(2 * 256 * sizeof(float2) <= L::kTileBytes, "the copies of (m, l) lie where the second Q tile would be");
+        float2* ml = reinterpret_cast<float2*>(smem + L::kQ + L::kTileBytes) + order.sums(joins) * 256;
         ml[half * 128 + row] = make_float2(m, l);
         warp_arrive_tc(&bars[L::bJoin]);
         if (!warp_wait(&bars[L::bJoin], joins & 1, abort_flag, kDevTimeoutSoftmax, 28 + half, (int)joins)) goto done;

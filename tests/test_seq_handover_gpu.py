@@ -51,3 +51,14 @@ def test_one_warp_moves_its_maximum_late(group):
         keep = torch.ones(500, 500, dtype=torch.bool).tril()
         for h in (0, 3, 5):
             U.check_attention(f"sequence {s} head {h}", o[h, t], lse[h, t], q[h, t], k[h // 4, t], v[h // 4, t], q.dtype, q.dtype, keep)
+
+
+@pytest.mark.parametrize("d,heads", [(128, 10), (64, 11)])
+def test_split_items_that_end_in_one_tile(d, heads):
+    # Key tiles split between the halves (under 300 items of 256 rows, 512 tokens a sequence and more): a block's last
+    # items have one key tile, of which the second half has none. Some 600 items, about four a block.
+    lens = [128 * 3 + 1] + [640, 1] * 3 + [1300, 2900]
+    q, k, v, ss = make(52, lens, heads, heads, d, torch.float16)
+    assert sum(lens) >= 512 * len(lens)
+    o, lse = forward(q, k, v, ss)
+    verify(o, lse, q, k, v, lens, heads=[0, heads - 1])

@@ -5,7 +5,7 @@ warpgroups as warps of their own, with barriers that are waited for by parity as
 barrier's current phase has the other parity, be it one phase further or one phase behind). The order of the
 products and the waits that follow from it are the kernel's own, from csrc/clear_seq_order.h. Random
 schedules, with agents that stall for long, look for a wait that passes before its phase is complete, for an
-accumulator that is read before its last product.
+accumulator that is read before its last product, and for a half's sums that are read after they were replaced.
 """
 import ctypes
 import os
@@ -22,7 +22,7 @@ SOURCE = """
 #include "clear_seq_order.h"
 template <int B, bool S> struct X { static int f(int what, int nA, int nB, int x, int y) {
   const clear::PromptOrder<B, S> o{nA, nB};
-  return what == 0 ? o.place(x, y) : what == 1 ? o.alone() : what == 2 ? o.first(x) : o.looks_back(x, y);
+  return what == 0 ? o.place(x, y) : what == 1 ? o.alone() : what == 2 ? o.first(x) : what == 3 ? o.looks_back(x, y) : o.sums(x);
 } };
 extern "C" int order(int bufs, int split, int what, int nA, int nB, int x, int y) {
   return bufs == 2 ? (split ? X<2, true>::f(what, nA, nB, x, y) : X<2, false>::f(what, nA, nB, x, y))
@@ -67,6 +67,7 @@ class Block:
         self.o = [Bar(1), Bar(1)]
         self.join, self.joined = Bar(2 * WARPS), Bar(2 * WARPS)
         self.pipe = []
+        self.ml = {}
         self.acc = [[], []]   # key tiles whose P V has been added to each accumulator, (item, tile)
 
     def counts(self, it):
@@ -148,10 +149,15 @@ class Block:
                     raise Fault(f"the accumulator of {half} is read at {self.acc[half][-1]} and not {(n, m - 1)}")
                 yield
                 continue
+            copy = self.order(4, it, joins)
+            self.ml[copy, half, w] = n
+            yield
             self.join.arrive()
             yield from self.wait("join", self.join, joins)
             yield
             joins += 1
+            if self.ml[copy, 1 - half, w] != n:
+                raise Fault(f"half {half} of item {n} reads the other's sums of item {self.ml[copy, 1 - half, w]}")
             for h in (0, 1):
                 k = self.counts(it)[h]
                 if k and self.acc[h][-1] != (n, k - 1):
