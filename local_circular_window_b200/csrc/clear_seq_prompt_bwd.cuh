@@ -79,8 +79,19 @@ __global__ void __launch_bounds__(kStatsThreads) clear_seq_bwd_stats_kernel(cons
   const long long row = ((long long)blockIdx.x * kStatsThreads + threadIdx.x) / kLanes;  // token-major: heads are next to each other
   const long long t = row / p.q_heads;
   const int h = (int)(row - t * p.q_heads);
+  // Rows behind the last sequence are left out. Where the offsets do not ascend, the last one need not be the largest: warps that
+  // reach behind it look for the sequence that ends last.
   int end = __ldg(p.seq_start + p.n_seq);
   end = end >= 0 && end < p.n_tok ? end : p.n_tok;
+  if (__any_sync(0xffffffffu, t >= end && t < p.n_tok)) {
+    int top = end;
+    for (int s = threadIdx.x & 31; s < p.n_seq; s += 32) {
+      int first, len;
+      seq_range(p.seq_start, p.n_tok, s, &first, &len);
+      top = first + len > top ? first + len : top;
+    }
+    end = __reduce_max_sync(0xffffffffu, top);
+  }
   const bool in = t < end;
   float sum = 0.f;
   if (in) {
