@@ -623,16 +623,17 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
 template <typename E, int D>
 __global__ void __launch_bounds__(kStatsThreads) clear_seq_bwd_join_kernel(const __grid_constant__ SeqBwdParams p) {
   using T = typename E::type;
+  constexpr int kLanes = D / 8;
   const long long rows = (long long)p.kv_heads * p.n_tok;
   const long long i = (long long)blockIdx.x * kStatsThreads + threadIdx.x;
-  const int c = (int)(i % (D / 8));
-  const long long r = i / (D / 8);
-  if (r >= 2 * rows) return;
+  const int c = (int)(i % kLanes);
+  const long long r = i / kLanes;
   const bool one = r < rows;
   const long long row = one ? r : r - rows;
   const int h = (int)(row / p.n_tok);
-  const long long t = row - (long long)h * p.n_tok;
-  // Only rows that belong to a sequence have been summed: find it, as a token's sequence is found for the cache.
+  const int t = r < 2 * rows ? (int)(row - (long long)h * p.n_tok) : -1;
+  // Only rows that belong to a sequence have been summed. The search finds a row's sequence where the offsets ascend; the warp
+  // looks through the whole list for a row (of its 32 / kLanes) that the search has not placed: padding, or offsets out of order.
   int lo = 0, n = p.n_seq;
   while (n > 1) {
     const int m = n / 2;
@@ -645,7 +646,18 @@ __global__ void __launch_bounds__(kStatsThreads) clear_seq_bwd_join_kernel(const
   }
   int first, len;
   seq_range(p.seq_start, p.n_tok, lo, &first, &len);
-  if (t < first || t >= first + len) return;
+  bool in = t >= first && t < first + len;
+  const int lane = threadIdx.x & 31;
+  for (unsigned lost = __ballot_sync(0xffffffffu, !in && t >= 0 && c == 0); lost; lost &= lost - 1) {
+    const int x = __shfl_sync(0xffffffffu, t, __ffs(lost) - 1);
+    bool found = false;
+    for (int s = lane; s < p.n_seq; s += 32) {
+      seq_range(p.seq_start, p.n_tok, s, &first, &len);
+      found = found || (x >= first && x < first + len);
+    }
+    if (__any_sync(0xffffffffu, found) && x == t) in = true;
+  }
+  if (!in) return;
   const float* src = (one ? p.part1 : p.part2) + (row * D + c * 8);
   float y[8] = {};
   for (int k = 0; k < p.parts; ++k) {

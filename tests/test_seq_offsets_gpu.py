@@ -24,8 +24,8 @@ BAD = [  # offsets, the sequences that remain
 
 
 @pytest.mark.parametrize("case", range(len(BAD)))
-@pytest.mark.parametrize("hq,hk,d,dtype", [(4, 4, 64, torch.bfloat16), (300, 300, 64, torch.float16)],
-                         ids=["few-items", "many-items"])
+@pytest.mark.parametrize("hq,hk,d,dtype", [(4, 4, 64, torch.bfloat16), (16, 1, 128, torch.float16), (300, 300, 64, torch.float16)],
+                         ids=["few-items", "parts", "many-items"])
 def test_gradients(case, hq, hk, d, dtype):
     bad, good = BAD[case]
     n = 350
