@@ -40,10 +40,11 @@ struct SeqAppendParams {
   double turns[kAppendMaxPairs];  // rate of pair i in turns per position: base^(-2i / rot) / (2 pi)
 };
 
-// The sequence that holds token t: the last s with seq_start[s] <= t, by a search in which the 32
-// lanes of a warp probe at once (one round for 32 sequences, two for 1024). -1 if t lies outside
-// of [seq_start[s], seq_start[s + 1]). Terminates whatever seq_start holds.
-__device__ __forceinline__ int seq_of_token(const int* __restrict__ seq_start, int n_seq, int t, int lane) {
+// The sequence that holds token t, or -1. Where the offsets ascend it is the last s with seq_start[s] <= t, found by a search in which
+// the 32 lanes of a warp probe at once (one round for 32 sequences, two for 1024). A token that the search has not placed
+// (padding, or offsets out of order) is looked for in the whole list. A sequence whose offsets decrease or leave [0, n_tok] holds no
+// token. Terminates whatever seq_start holds.
+__device__ __forceinline__ int seq_of_token(const int* __restrict__ seq_start, int n_seq, int n_tok, int t, int lane, int* end) {
   int lo = 0, n = n_seq;  // candidates [lo, lo + n)
   while (n > 1) {
     const int step = (n + 31) / 32;
@@ -54,7 +55,27 @@ __device__ __forceinline__ int seq_of_token(const int* __restrict__ seq_start, i
     lo += first;
     n = n - first < step ? n - first : step;
   }
-  return (__ldg(seq_start + lo) <= t && t < __ldg(seq_start + lo + 1)) ? lo : -1;
+  const int a = __ldg(seq_start + lo), b = __ldg(seq_start + lo + 1);
+  *end = b;
+  if (a >= 0 && a <= t && t < b && b <= n_tok) return lo;
+  int s = -1;
+  for (int i = lane; i < n_seq && s < 0; i += 32) {
+    const int c = __ldg(seq_start + i), e = __ldg(seq_start + i + 1);
+    if (c >= 0 && c <= t && t < e && e <= n_tok) s = i;
+  }
+  s = __reduce_max_sync(0xffffffffu, s);
+  if (s >= 0) *end = __ldg(seq_start + s + 1);
+  return s;
+}
+
+// Offsets that decrease or reach outside leave their sequence out: says so. One block's warps beside the first call it, while that one
+// follows its chain of loads. Not inlined: as a loop of the kernel's own it took 5 % of a long prompt's time (16384 tokens: 79.7 and
+// 76 us).
+__device__ __noinline__ void report_bad_offsets(const int* __restrict__ seq_start, int n_seq, int n_tok, int first, int step) {
+  for (int s = first; s < n_seq; s += step) {
+    const int a = __ldg(seq_start + s), b = __ldg(seq_start + s + 1);
+    if (a < 0 || b < a || b > n_tok) record_bad_index(kSiteSeqStart, s, a, b);
+  }
 }
 
 // E: element type; kF8: E4M3 cache; D: head dim; kHalves: pairs of halves.
@@ -88,9 +109,10 @@ __global__ void __launch_bounds__(kAppendMaxThreads) clear_seq_append_kernel(con
   if (tid < 32) {
     int pos = -1;
     long long kr = -1, vr = -1;
-    const int s = seq_of_token(p.seq_start, p.n_seq, t, lane);
+    int end;
+    const int s = seq_of_token(p.seq_start, p.n_seq, p.n_tok, t, lane, &end);
     if (s >= 0) {
-      const long long x = (long long)__ldg(p.seq_len + s) - ((long long)__ldg(p.seq_start + s + 1) - t);
+      const long long x = (long long)__ldg(p.seq_len + s) - (end - t);
       if (x >= 0) {  // a negative position is padding
         pos = (int)x;
         const int pg = p.c.page_div.div(pos);
@@ -109,6 +131,8 @@ __global__ void __launch_bounds__(kAppendMaxThreads) clear_seq_append_kernel(con
       row_at[0] = kr;
       row_at[1] = vr;
     }
+  } else if (blockIdx.x == 0) {
+    report_bad_offsets(p.seq_start, p.n_seq, p.n_tok, tid - 32, blockDim.x - 32);
   }
   __syncthreads();
   const int pos = pos_at;

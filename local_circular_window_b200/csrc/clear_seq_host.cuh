@@ -82,7 +82,7 @@ template <typename E, bool kF8, int D, bool kHalves>
 clear_status_t launch_append(const SeqAppendParams& a, cudaStream_t stream) {
   const int items = ((a.q_heads + 2 * a.kv_heads) * (D / 16) + 31) & ~31;
   const int most = a.n_tok >= kAppendMany ? 128 : kAppendMaxThreads;
-  clear_seq_append_kernel<E, kF8, D, kHalves><<<a.n_tok, items < most ? items : most, 0, stream>>>(a);
+  clear_seq_append_kernel<E, kF8, D, kHalves><<<a.n_tok, items < 64 ? 64 : items < most ? items : most, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? CLEAR_OK : CLEAR_ERR_CUDA;
 }
 

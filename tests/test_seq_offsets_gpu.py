@@ -25,7 +25,7 @@ BAD = [  # offsets, the sequences that remain
 
 @pytest.mark.parametrize("case", range(len(BAD)))
 @pytest.mark.parametrize("hq,hk,d,dtype", [(4, 4, 64, torch.bfloat16), (16, 1, 128, torch.float16), (300, 300, 64, torch.float16)],
-                         ids=["few-items", "parts", "many-items"])
+                         ids=["group1", "parts", "no-parts"])
 def test_gradients(case, hq, hk, d, dtype):
     bad, good = BAD[case]
     n = 350
@@ -54,3 +54,42 @@ def test_gradients(case, hq, hk, d, dtype):
             assert torch.equal(x[:, a:b], y[:, a:b])
     for x in got:
         assert (x[:, ~seen.cuda()] == 7).all()  # rows of no sequence
+
+
+@pytest.mark.parametrize("case", range(len(BAD)))
+@pytest.mark.parametrize("hq,hk", [(0, 1), (4, 2)], ids=["one-warp", "warps"])
+def test_append(case, hq, hk):
+    bad, good = BAD[case]
+    n, d, page = 350, 64, 16
+    gen = torch.Generator().manual_seed(case)
+    lens = [400] * (len(bad) - 1)
+    kp, vp, table = (x.cuda() for x in U.pages(gen, lens, page, hk, d, torch.bfloat16))
+    k, v = (U.packed(gen, hk, n, d, torch.bfloat16).cuda() for _ in range(2))
+    q = U.packed(gen, hq, n, d, torch.bfloat16).cuda() if hq else None
+    k_out = torch.full_like(k, 7.0)
+    a, b = kp.clone(), vp.clone()
+    L.clear_attn_cache_append(k, v, a, b, table, ints(bad), ints(lens), q=q, k_out=k_out, rot=32)
+    assert L.clear_attn_check() == 6 and L.clear_attn_check() == 0
+    want_k, want_v, want_out = kp.clone(), vp.clone(), torch.full_like(k, 7.0)
+    for s in good:  # each alone: its new tokens are the last of 400
+        t = slice(bad[s], bad[s + 1])
+        part = torch.empty_like(k[:, t])
+        L.clear_attn_cache_append(k[:, t], v[:, t], want_k, want_v, table[s:s + 1], ints([0, t.stop - t.start]), ints([400]), k_out=part, rot=32)
+        want_out[:, t] = part
+    assert L.clear_attn_check() == 0
+    assert torch.equal(a, want_k) and torch.equal(b, want_v) and torch.equal(k_out, want_out)
+
+
+def test_tokens_of_two_sequences_stay_inside():
+    # Rows 40 to 49 belong to two sequences: what they get is not defined, all others are.
+    n, d = 150, 64
+    gen = torch.Generator().manual_seed(3)
+    kp, vp, table = (x.cuda() for x in U.pages(gen, [200] * 3, 16, 1, d, torch.bfloat16))
+    k, v = (U.packed(gen, 1, n, d, torch.bfloat16).cuda() for _ in range(2))
+    a, b = kp.clone(), vp.clone()
+    L.clear_attn_cache_append(k, v, a, b, table, ints([0, 50, 40, 150]), ints([200] * 3))
+    assert L.clear_attn_check() == 6
+    rows = lambda x, s: x[table[s, :13].long()].flatten(0, 1)[:200, 0]  # noqa: E731
+    assert torch.equal(rows(a, 0)[150:190], k[0, :40]) and torch.equal(rows(a, 2)[100:], k[0, 50:])
+    assert torch.equal(rows(b, 0)[150:190], v[0, :40]) and torch.equal(rows(b, 2)[100:], v[0, 50:])
+    assert torch.equal(rows(a, 1), rows(kp, 1))
