@@ -363,10 +363,11 @@ CLEAR_API clear_status_t clear_attn_bwd(const clear_attn_params_t* params, const
                               void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
                               void* stream);
 
-/* Synchronises `stream`, then reads and clears the device error word of the current device.
+/* Synchronises `stream`, then reads and clears a device error word of the current device.
  * Returns CLEAR_OK, CLEAR_ERR_DEVICE_TIMEOUT (a kernel gave up a bounded wait; its outputs are
  * invalid), CLEAR_ERR_DEVICE_INDEX (a token-sequence operator met an index out of range in device
- * memory) or CLEAR_ERR_CUDA (the stream reported a CUDA error). */
+ * memory) or CLEAR_ERR_CUDA (the stream reported a CUDA error). Expired waits and bad indexes have a
+ * word each: where both are set, this call reports the wait and the next one the index. */
 CLEAR_API clear_status_t clear_attn_check(void* stream);
 
 /* Context of the expired wait or bad index behind the last CLEAR_ERR_DEVICE_TIMEOUT or

@@ -1169,17 +1169,15 @@ static thread_local int t_last_diag[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 
 clear_status_t clear_attn_check(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return CLEAR_ERR_CUDA;
-  int err = 0;
-  if (cudaMemcpyFromSymbol(&err, clear::g_clear_device_error, sizeof(int)) != cudaSuccess)
+  int err[2] = {0, 0};
+  if (cudaMemcpyFromSymbol(err, clear::g_clear_device_error, sizeof(err)) != cudaSuccess) return CLEAR_ERR_CUDA;
+  const int which = err[clear::kDevWait] != 0 ? clear::kDevWait : clear::kDevIndex;
+  if (err[which] == 0) return CLEAR_OK;
+  if (cudaMemcpyFromSymbol(t_last_diag, clear::g_clear_device_diag, sizeof(t_last_diag), which * sizeof(t_last_diag)) != cudaSuccess)
     return CLEAR_ERR_CUDA;
-  if (err != 0) {
-    if (cudaMemcpyFromSymbol(t_last_diag, clear::g_clear_device_diag, sizeof(t_last_diag)) != cudaSuccess)
-      return CLEAR_ERR_CUDA;
-    const int zero = 0;
-    cudaMemcpyToSymbol(clear::g_clear_device_error, &zero, sizeof(int));
-    return err == clear::kDevBadIndex ? CLEAR_ERR_DEVICE_INDEX : CLEAR_ERR_DEVICE_TIMEOUT;
-  }
-  return CLEAR_OK;
+  const int zero = 0;
+  cudaMemcpyToSymbol(clear::g_clear_device_error, &zero, sizeof(int), which * sizeof(int));
+  return which == clear::kDevWait ? CLEAR_ERR_DEVICE_TIMEOUT : CLEAR_ERR_DEVICE_INDEX;
 }
 
 void clear_attn_device_diag(int* out8) {

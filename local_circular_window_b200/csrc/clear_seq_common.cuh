@@ -5,7 +5,7 @@
 // sequence s has the tokens [seq_start[s], seq_start[s + 1]). Offsets, lengths and page numbers live
 // in device memory, so a captured graph can be replayed with others; the host cannot check them.
 // Every kernel therefore checks each one before it is used as an address: a bad one is skipped and
-// recorded in the device error word (kDevBadIndex, reported by clear_attn_check()).
+// recorded in a device error word of its own (kDevBadIndex, reported by clear_attn_check()).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -19,15 +19,16 @@ enum SeqSite : int { kSiteAppendPage = 32, kSiteDecodePage = 33, kSiteSeqStart =
 
 // Records a length, offset or page number out of range: the first one wins.
 __device__ __noinline__ void record_bad_index(int site, int c0, int c1, int c2) {
-  if (atomicCAS(&g_clear_device_error, 0, (int)kDevBadIndex) == 0) {
-    g_clear_device_diag[0] = kDevBadIndex;
-    g_clear_device_diag[1] = site;
-    g_clear_device_diag[2] = blockIdx.x;
-    g_clear_device_diag[3] = threadIdx.x;
-    g_clear_device_diag[4] = 0;
-    g_clear_device_diag[5] = c0;
-    g_clear_device_diag[6] = c1;
-    g_clear_device_diag[7] = c2;
+  if (atomicCAS(&g_clear_device_error[kDevIndex], 0, (int)kDevBadIndex) == 0) {
+    int* const diag = g_clear_device_diag[kDevIndex];
+    diag[0] = kDevBadIndex;
+    diag[1] = site;
+    diag[2] = blockIdx.x;
+    diag[3] = threadIdx.x;
+    diag[4] = 0;
+    diag[5] = c0;
+    diag[6] = c1;
+    diag[7] = c2;
     __threadfence();
   }
 }

@@ -8,8 +8,9 @@
 namespace clear {
 
 // ------------------------------------------------------------------------------------------------
-// Device error word. Kernels set it when a bounded wait expires (or on an internal consistency
-// failure); the host reads and clears it in clear_attn_check().
+// Device error words. Kernels set one when a bounded wait expires (or on an internal consistency
+// failure) and the other when they skip a bad index; the host reads and clears them in clear_attn_check(),
+// the expired wait first: its outputs are invalid, and no bad index may hide that.
 // ------------------------------------------------------------------------------------------------
 enum DeviceError : int {
   kDevOk = 0,
@@ -21,10 +22,12 @@ enum DeviceError : int {
   kDevBadIndex = 16,  // an index held in device memory was out of range and was skipped
 };
 
+constexpr int kDevWait = 0, kDevIndex = 1;  // words and records below: expired waits, bad indexes
+
 // Defined once per library (single translation unit).
-__device__ int g_clear_device_error = 0;
-// Context of the first expired wait: {code, site, block, thread, parity, ctx0, ctx1, ctx2}.
-__device__ int g_clear_device_diag[8];
+__device__ int g_clear_device_error[2] = {0, 0};
+// Context of the first expired wait and of the first bad index: {code, site, block, thread, parity, ctx0, ctx1, ctx2}.
+__device__ int g_clear_device_diag[2][8];
 // The same record for the first expiry at each wait site (0..31), for diagnosis.
 __device__ int g_clear_device_diag_sites[32][8];
 
@@ -42,15 +45,16 @@ __device__ __forceinline__ void record_timeout(volatile int* abort_flag, int err
     g_clear_device_diag_sites[si][6] = c1;
     g_clear_device_diag_sites[si][7] = c2;
   }
-  if (atomicCAS(&g_clear_device_error, 0, err_code) == 0) {
-    g_clear_device_diag[0] = err_code;
-    g_clear_device_diag[1] = site;
-    g_clear_device_diag[2] = blockIdx.x;
-    g_clear_device_diag[3] = threadIdx.x;
-    g_clear_device_diag[4] = parity;
-    g_clear_device_diag[5] = c0;
-    g_clear_device_diag[6] = c1;
-    g_clear_device_diag[7] = c2;
+  if (atomicCAS(&g_clear_device_error[kDevWait], 0, err_code) == 0) {
+    int* const diag = g_clear_device_diag[kDevWait];
+    diag[0] = err_code;
+    diag[1] = site;
+    diag[2] = blockIdx.x;
+    diag[3] = threadIdx.x;
+    diag[4] = parity;
+    diag[5] = c0;
+    diag[6] = c1;
+    diag[7] = c2;
     __threadfence();
   }
 }

@@ -93,3 +93,20 @@ def test_tokens_of_two_sequences_stay_inside():
     assert torch.equal(rows(a, 0)[150:190], k[0, :40]) and torch.equal(rows(a, 2)[100:], k[0, 50:])
     assert torch.equal(rows(b, 0)[150:190], v[0, :40]) and torch.equal(rows(b, 2)[100:], v[0, 50:])
     assert torch.equal(rows(a, 1), rows(kp, 1))
+
+
+def test_expired_wait_is_not_hidden_by_a_bad_page():
+    # A bad index and an expired wait before one look: the expired wait, whose outputs are invalid, is told first.
+    gen = torch.Generator().manual_seed(4)
+    q = U.packed(gen, 1, 1, 64, torch.bfloat16).cuda()
+    kp, vp, table = (x.cuda() for x in U.pages(gen, [20], 16, 1, 64, torch.bfloat16))
+    table[0, 0] = -5
+    for first in (False, True):
+        if first:
+            assert L.selftest_expiry(20) == 0
+        L.clear_attn_decode(q, kp, vp, table, ints([20]))
+        if not first:
+            assert L.selftest_expiry(20) == 0
+        assert L.clear_attn_check() == 5 and L.device_diag()[:2] == [5, 31]
+        assert L.clear_attn_check() == 6 and L.device_diag()[:2] == [16, 33]
+        assert L.clear_attn_check() == 0
