@@ -74,14 +74,22 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // 16-bit element types: one pair per 32-bit register, the lower half first.
+//
+// kLift: probabilities relative to the maximum in use, which may be 2^8 below the true one, are held times 2^kLift.
+// bf16 has fp32's exponents: each is rounded by half a step, 2^-8 of itself at most, however small. fp16's steps are absolute below
+// 2^-14: plain probabilities would be off by up to 2^-25 of the largest key's weight each, all with one sign where many keys are
+// alike. Times 2^7 they stay below 2^15, half a step is 2^-11 of each down to 2^-21 of the largest weight, and an
+// absolute 2^-32 of it below: 2^-15 in all from 131072 keys.
 struct Bf16 {
   using type = __nv_bfloat16;
+  static constexpr float kLift = 0.f;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
   static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
   static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 };
 struct Fp16 {
   using type = __half;
+  static constexpr float kLift = 7.f;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

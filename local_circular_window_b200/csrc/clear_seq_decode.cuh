@@ -30,8 +30,8 @@
 // Both leave the 128-byte (64-byte) swizzle that keeps ldmatrix free of bank conflicts. Value rows past
 // the sequence's end are cleared before use, so what a page holds behind the last token
 // (NaN included) does not count. Softmax statistics and sums are fp32; probabilities are rounded
-// to the matrix instruction's 16-bit type (bf16, or fp16 for fp16 and E4M3 caches: half a step,
-// 2^-8 or 2^-11 of each at most, of random sign).
+// to the matrix instruction's 16-bit type (bf16, or fp16 for fp16 and E4M3 caches: half a step, 2^-8 or 2^-11 of each at
+// most; fp16 holds them times 2^7, see Fp16::kLift).
 //
 // E4M3 caches: codes are widened exactly to fp16 after ldmatrix; the keys' scale goes into the score
 // scale, the values' into the output. The codes of one 32-bit register belong to four neighbouring elements of d
@@ -216,6 +216,7 @@ __global__ void __launch_bounds__(kDecThreads, DecLayout<kF8, D, kN>::kPerSm) cl
   using T = typename E::type;
   using L = DecLayout<kF8, D, kN>;
   constexpr bool kHalf = kF8 || !std::is_same<E, Bf16>::value;  // the matrix instruction's 16-bit type
+  constexpr float kLift = kHalf ? Fp16::kLift : Bf16::kLift;
   constexpr int kSteps = D / 16;
   extern __shared__ __align__(1024) uint8_t dsm[];
   // All shared memory is dynamic: static arrays would sit before it, padded to its alignment.
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(kDecThreads, DecLayout<kF8, D, kN>::kPerSm) cl
           float e[2];
           #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            e[u] = ex2_approx(c[n][2 * r + u] - (m[n][u] == -INFINITY ? 0.f : m[n][u]));
+            e[u] = ex2_approx(c[n][2 * r + u] - ((m[n][u] == -INFINITY ? 0.f : m[n][u]) - kLift));
             l[n][u] += e[u];
           }
           pb[n][r] = movmatrix(kHalf ? Fp16::pack(e[0], e[1]) : Bf16::pack(e[0], e[1]));
@@ -562,7 +563,7 @@ __global__ void __launch_bounds__(kDecThreads, DecLayout<kF8, D, kN>::kPerSm) cl
       #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int row = warp * L::kRows + n * 8 + 2 * t + u;
-        if (g == 0) jml[row] = make_float2(m[n][u], l[n][u]);
+        if (g == 0) jml[row] = make_float2(m[n][u] - kLift, l[n][u]);  // l and O have the factor 2^kLift
         #pragma unroll
         for (int j = 0; j < kSteps; ++j) {
           float* d = jo + row * D + j * 16;

@@ -31,7 +31,7 @@
 //
 // The running maximum is followed lazily: O and the sum are rescaled only when a row's maximum has
 // grown by more than 2^8, which changes nothing but rounding. P is rounded to the element type for
-// the second product (half a step of each probability, of random sign); sums are of the unrounded values.
+// the second product (half a step of each probability; fp16 holds them times 2^7, see Fp16::kLift); sums are of the unrounded values.
 //
 // Value rows behind the sequence's end belong to the next sequence or to nothing. Their
 // probabilities are zero, but 0 * NaN is not: the threads of the tile that uses them (the diagonal's)
@@ -526,7 +526,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
             w[e] = E::pack(p0, p1);
           }
         };
-        float base = m == -INFINITY ? 0.f : m;
+        float base = (m == -INFINITY ? 0.f : m) - E::kLift;
         probabilities(a0, base, w0);
         probabilities(a1, base, w1);
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -568,7 +568,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
           cut(a0, 0);
           cut(a1, 32);
           sum[0] = sum[1] = 0;
-          base = m == -INFINITY ? 0.f : m;
+          base = (m == -INFINITY ? 0.f : m) - E::kLift;
           probabilities(a0, base, w0);
           probabilities(a1, base, w1);
         }
@@ -625,7 +625,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
           tmem_wait_ld(ov);
           if (valid) store32(ov, inv, c);
         }
-        if (valid && p.lse) p.lse[(long long)it.w * p.n_tok + tok] = (m + log2f(l)) * 0.69314718055994530942f;
+        if (valid && p.lse) p.lse[(long long)it.w * p.n_tok + tok] = (m - E::kLift + log2f(l)) * 0.69314718055994530942f;
       } else {
         static_assert(2 * 256 * sizeof(float2) <= L::kTileBytes, "the copies of (m, l) lie where the second Q tile would be");
         float2* ml = reinterpret_cast<float2*>(smem + L::kQ + L::kTileBytes) + order.sums(joins) * 256;
@@ -657,7 +657,7 @@ clear_seq_prompt_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __gr
           }
           if (valid) store32(ov, 1.f, c);
         }
-        if (valid && half == 0 && p.lse) p.lse[(long long)it.w * p.n_tok + tok] = (top + log2f(sum)) * 0.69314718055994530942f;
+        if (valid && half == 0 && p.lse) p.lse[(long long)it.w * p.n_tok + tok] = (top - E::kLift + log2f(sum)) * 0.69314718055994530942f;
         warp_arrive_tc(&bars[L::bJoined]);
       }
       tc_fence_before();  // before the next item's first P: its P V overwrites O
