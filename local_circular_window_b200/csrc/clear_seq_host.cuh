@@ -11,6 +11,25 @@
 
 namespace {
 
+// Launches a kernel as a programmatic dependent of the one before it in the stream: it may start early and waits for that one's
+// results by griddepcontrol.wait.
+template <typename... P, typename... A>
+bool launch_dependent(void (*kernel)(P...), dim3 grid, int block, int smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
 // Allows a kernel `bytes` of dynamic shared memory, once per device: `done` has a bit for each of the first 64.
 bool allow_smem(const void* kernel, int bytes, std::atomic<unsigned long long>* done) {
   int dev = 0;
@@ -141,20 +160,8 @@ clear_status_t launch_decode(SeqDecodeParams p, int num_sms, cudaStream_t stream
   const int blocks = resident < kDecMaxBlocks ? resident : kDecMaxBlocks;
   kernel<<<blocks, kDecThreads, smem, stream>>>(mk, mv, p);
   if (cudaGetLastError() != cudaSuccess) return CLEAR_ERR_CUDA;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks, p.group < kDecRows ? p.group : kDecRows);
-  cfg.blockDim = dim3(kJoinParts * D);
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, clear_seq_decode_join_kernel<E, D>, p) != cudaSuccess) {
-    cudaGetLastError();
-    return CLEAR_ERR_CUDA;
-  }
-  return CLEAR_OK;
+  const dim3 join(blocks, p.group < kDecRows ? p.group : kDecRows);
+  return launch_dependent(clear_seq_decode_join_kernel<E, D>, join, kJoinParts * D, 0, stream, p) ? CLEAR_OK : CLEAR_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------------------------------- prompt
@@ -211,17 +218,22 @@ int bwd_parts(const clear_seq_params_t* p) {
 }
 
 struct PromptBwdWorkspace {
-  size_t part1_off, part2_off, total;
+  size_t norm_g_off, norm_v_off, range_off, part1_off, part2_off, total;
 };
 PromptBwdWorkspace prompt_bwd_workspace_layout(const clear_seq_params_t* p) {
   PromptBwdWorkspace w;
   const int parts = bwd_parts(p);
   const size_t sums = parts > 1 ? (size_t)parts * p->kv_heads * p->n_tok * p->d * sizeof(float) : 0;
-  w.part1_off = align256((size_t)p->q_heads * p->n_tok * sizeof(float2));
+  w.norm_g_off = align256((size_t)p->q_heads * p->n_tok * sizeof(float2));  // (-lse, -D) before
+  w.norm_v_off = w.norm_g_off + align256((size_t)p->q_heads * p->n_tok * sizeof(float));
+  w.range_off = w.norm_v_off + align256((size_t)p->kv_heads * p->n_tok * sizeof(float));
+  w.part1_off = w.range_off + align256((size_t)p->kv_heads * p->n_tok * sizeof(float2));
   w.part2_off = w.part1_off + align256(sums);
   w.total = w.part2_off + align256(sums);
   return w;
 }
+
+constexpr int kRangeBlocks = 1024;  // along the sequences
 
 template <typename E, int D>
 clear_status_t launch_prompt_bwd(const clear_seq_params_t* sp, const SeqView& q, const SeqView& k, const SeqView& v, const SeqView& g,
@@ -240,12 +252,21 @@ clear_status_t launch_prompt_bwd(const clear_seq_params_t* sp, const SeqView& q,
   if (!allow_smem(reinterpret_cast<const void*>(clear_seq_prompt_bwd_kernel<E, D, true>), LK::kAlloc, &done[0]) ||
       !allow_smem(reinterpret_cast<const void*>(clear_seq_prompt_bwd_kernel<E, D, false>), LQ::kAlloc, &done[1]))
     return CLEAR_ERR_CUDA;
+  constexpr bool kF16 = !std::is_same<E, Bf16>::value;
   const long long lanes = (long long)sp->n_tok * sp->q_heads * (D / 8);
   clear_seq_bwd_stats_kernel<E, D><<<(unsigned)((lanes + kStatsThreads - 1) / kStatsThreads), kStatsThreads, 0, stream>>>(st);
   if (cudaGetLastError() != cudaSuccess) return CLEAR_ERR_CUDA;
   p.out2 = dq;  // first: it settles the first rows' statistics for the other
-  clear_seq_prompt_bwd_kernel<E, D, false><<<prompt_blocks(sp, 128, sp->q_heads, num_sms), kPrThreads, LQ::kAlloc, stream>>>(mq, mg, sk, sv, p);
-  if (cudaGetLastError() != cudaSuccess) return CLEAR_ERR_CUDA;
+  const unsigned q_blocks = prompt_blocks(sp, 128, sp->q_heads, num_sms);
+  if (kF16) {
+    const dim3 range(sp->n_seq < kRangeBlocks ? sp->n_seq : kRangeBlocks, sp->kv_heads);
+    if (!launch_dependent(clear_seq_bwd_range_kernel, range, kRangeThreads, 0, stream, p) ||
+        !launch_dependent(clear_seq_prompt_bwd_kernel<E, D, false>, q_blocks, kPrThreads, LQ::kAlloc, stream, mq, mg, sk, sv, p))
+      return CLEAR_ERR_CUDA;
+  } else {
+    clear_seq_prompt_bwd_kernel<E, D, false><<<q_blocks, kPrThreads, LQ::kAlloc, stream>>>(mq, mg, sk, sv, p);
+    if (cudaGetLastError() != cudaSuccess) return CLEAR_ERR_CUDA;
+  }
   p.out1 = dv;
   p.out2 = dk;
   clear_seq_prompt_bwd_kernel<E, D, true><<<prompt_blocks(sp, 128, sp->kv_heads * p.parts, num_sms), kPrThreads, LK::kAlloc, stream>>>(mk, mv, sq, sg, p);
@@ -409,11 +430,15 @@ clear_status_t clear_attn_prompt_bwd(const clear_seq_params_t* params, const int
   SeqStatsParams sp{};
   sp.o = w[3];
   sp.g = w[4];
+  sp.v = w[2];
   sp.lse = lse;
   sp.stats = static_cast<float2*>(workspace);
   SeqBwdParams p{};
   p.stats = sp.stats;
   const PromptBwdWorkspace wl = prompt_bwd_workspace_layout(params);
+  p.norm_g = sp.norm_g = reinterpret_cast<float*>(static_cast<char*>(workspace) + wl.norm_g_off);
+  p.norm_v = sp.norm_v = reinterpret_cast<float*>(static_cast<char*>(workspace) + wl.norm_v_off);
+  p.range = reinterpret_cast<float2*>(static_cast<char*>(workspace) + wl.range_off);
   p.parts = bwd_parts(params);
   p.part1 = reinterpret_cast<float*>(static_cast<char*>(workspace) + wl.part1_off);
   p.part2 = reinterpret_cast<float*>(static_cast<char*>(workspace) + wl.part2_off);
@@ -422,7 +447,7 @@ clear_status_t clear_attn_prompt_bwd(const clear_seq_params_t* params, const int
   p.n_tok = sp.n_tok = params->n_tok;
   p.q_heads = sp.q_heads = params->q_heads;
   p.kv_heads = params->kv_heads;
-  p.group = params->q_heads / params->kv_heads;
+  p.group = sp.group = params->q_heads / params->kv_heads;
   p.scale = (float)(1.0 / std::sqrt((double)params->d));
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)params->d));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -3,8 +3,9 @@
 //   P = e^(S - lse), S = Q K^T / sqrt(d);  D_i = sum dO_i o_i;  dP = dO V^T;  dS = P (dP - D);
 //   dV = P^T dO,  dK = dS^T Q / sqrt(d), both summed over the query heads of the group;  dQ = dS K / sqrt(d).
 //
-// Three launches, deterministic, without atomics:
-//   stats   (-lse, -D) of every row, one pass over o and dO (bound by memory)
+// Three launches (fp16: four), deterministic, without atomics:
+//   stats   (-lse, -D) of every row, one pass over o and dO (bound by memory); fp16: norms of dO's and v's rows
+//   range   fp16: the largest norms of each sequence and kv head
 //   q       one item per 128-row query tile and query head: Q and dO stay, K and V stream past
 //   kv      one item per 128-key tile and kv head: K and V stay, the group's Q and dO stream past
 // S and dP are computed in both, seven products in place of five: the price of writing every gradient
@@ -31,7 +32,14 @@
 // three parts each of 16-bit type, whose products with the constants add up to the fp32 value (24 bits
 // and more). P = 2^(S' log2 e / sqrt(d)) and dS = P dP' then need no other input.
 //
-// Rounding P and dS costs half a step of each, of random sign; sums, statistics and accumulators are fp32.
+// P and dS are rounded to the element type; sums, statistics and accumulators are fp32. In bf16 that is half a step of each, 2^-8
+// at most. fp16's steps are absolute below 2^-14, where P (about 1 / keys) and dS = P (dP - D) of small gradients lie, and its
+// range ends at 2^16. So fp16 holds P times 2^14 (P <= 1), and dS times a power of two from the bound
+//   |dS_ij| <= |dP_ij| + |D_i| <= 2 |dO_i| |v|max   (norms of rows; |v|max over the sequence and kv head)
+// that brings the bound to 2^13 ... 2^14: one per row in the q kernel, one per sequence and kv head (with the largest |dO_i| of the
+// group's heads) in kv. Both are taken out again from the fp32 accumulators. dS of any fp16 input is then in range, and half a
+// step is 2^-11 of each down to 2^-27 of its bound, an absolute 2^-38 of the bound below. The norms ride along in the statistics' pass; a
+// small kernel finds their maxima.
 //
 // D from the given o carries o's rounding, which dS = P (dP - D) shares along the whole row: against the
 // rounding of dS itself that is about one part in sqrt(keys), so it shows only in a sequence's first
@@ -55,27 +63,43 @@ struct SeqBwdParams {
   int parts;
   float *part1, *part2;
   float2* stats;         // [q_heads, n_tok]: (-lse, -D)
+  // fp16: norms of the rows of dO [q_heads, n_tok] and of v [kv_heads, n_tok]; the largest of each in a sequence (of dO: of the
+  // group's heads) [kv_heads, n_tok], at the sequence's first token.
+  float *norm_g, *norm_v;
+  float2* range;
   const int* seq_start;
   int n_seq, n_tok, q_heads, kv_heads, group;
   float scale, scale_log2;
 };
 
+// The power of two that brings 2 a b, the bound of |dS| of rows with norms a and b, to [2^13, 2^14). Zero, infinite and NaN bounds
+// stay: such rows hold nothing that could be kept.
+__device__ __forceinline__ int lift_of(float a, float b) {
+  const float bound = 2.f * a * b;
+  return bound > 0.f && bound < INFINITY ? 13 - ilogbf(bound) : 0;
+}
+constexpr float kBwdLift = 14.f;  // fp16: P is held times 2^14
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }  // -126 <= e <= 127
+
 struct SeqStatsParams {
-  SeqView o, g;
+  SeqView o, g, v;
   const float* lse;
   float2* stats;
+  float *norm_g, *norm_v;
   const int* seq_start;
-  int n_seq, n_tok, q_heads;
+  int n_seq, n_tok, q_heads, group;
 };
 
 constexpr int kStatsThreads = 256;
 
-// D / 8 lanes take one row of o and dO.
+// D / 8 lanes take one row of o and dO, in fp16 those of a group's first head also one of v.
 template <typename E, int D>
 __global__ void __launch_bounds__(kStatsThreads) clear_seq_bwd_stats_kernel(const __grid_constant__ SeqStatsParams p) {
   using T = typename E::type;
   constexpr int kLanes = D / 8;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x % kLanes;
+  constexpr bool kNorms = !std::is_same<E, Bf16>::value;
   const long long row = ((long long)blockIdx.x * kStatsThreads + threadIdx.x) / kLanes;  // token-major: heads are next to each other
   const long long t = row / p.q_heads;
   const int h = (int)(row - t * p.q_heads);
@@ -93,20 +117,77 @@ __global__ void __launch_bounds__(kStatsThreads) clear_seq_bwd_stats_kernel(cons
     end = __reduce_max_sync(0xffffffffu, top);
   }
   const bool in = t < end;
-  float sum = 0.f;
+  const int hk = kNorms ? h / p.group : 0;
+  const bool first = kNorms && h == hk * p.group;
+  float sum = 0.f, square_g = 0.f, square_v = 0.f;
   if (in) {
     const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.o.ptr) + h * p.o.sh + t * p.o.st) + lane);
     const uint4 b = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.g.ptr) + h * p.g.sh + t * p.g.st) + lane);
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+    uint4 c = make_uint4(0, 0, 0, 0);
+    if (first) c = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.v.ptr) + hk * p.v.sh + t * p.v.st) + lane);
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w}, z[4] = {c.x, c.y, c.z, c.w};
     #pragma unroll
-    for (int e = 0; e < 4; ++e) sum = fmaf(E::hi(x[e]), E::hi(y[e]), fmaf(E::lo(x[e]), E::lo(y[e]), sum));
+    for (int e = 0; e < 4; ++e) {
+      sum = fmaf(E::hi(x[e]), E::hi(y[e]), fmaf(E::lo(x[e]), E::lo(y[e]), sum));
+      if (kNorms) {
+        square_g = fmaf(E::hi(y[e]), E::hi(y[e]), fmaf(E::lo(y[e]), E::lo(y[e]), square_g));
+        square_v = fmaf(E::hi(z[e]), E::hi(z[e]), fmaf(E::lo(z[e]), E::lo(z[e]), square_v));
+      }
+    }
   }
   #pragma unroll
-  for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  for (int d = kLanes / 2; d > 0; d >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (kNorms) {
+      square_g += __shfl_xor_sync(0xffffffffu, square_g, d);
+      square_v += __shfl_xor_sync(0xffffffffu, square_v, d);
+    }
+  }
   if (in && lane == 0) {
     const float l = __ldg(p.lse + (long long)h * p.n_tok + t);
     // A row without a finite score (lse -inf) has P = 0: 2^(-inf) instead of 2^(-inf + inf).
     p.stats[(long long)h * p.n_tok + t] = make_float2(l == -INFINITY ? -INFINITY : -l, -sum);
+    if (kNorms) p.norm_g[(long long)h * p.n_tok + t] = sqrtf(square_g);
+    if (first) p.norm_v[(long long)hk * p.n_tok + t] = sqrtf(square_v);
+  }
+}
+
+// The largest norms of a sequence's rows: a block takes one sequence and kv head at a time. Whether a NaN takes part does not matter.
+// It and the q kernel behind it are programmatic dependents: their launches hide behind the kernel before.
+constexpr int kRangeThreads = 512;
+__global__ void __launch_bounds__(kRangeThreads) clear_seq_bwd_range_kernel(const __grid_constant__ SeqBwdParams p) {
+  __shared__ float2 best[kRangeThreads / 32];
+  const int hk = blockIdx.y, tid = threadIdx.x;
+  asm volatile("griddepcontrol.wait;\ngriddepcontrol.launch_dependents;" ::: "memory");
+  for (int s = blockIdx.x; s < p.n_seq; s += gridDim.x) {
+    int first, len;
+    seq_range(p.seq_start, p.n_tok, s, &first, &len);
+    if (len == 0) continue;
+    float g = 0.f, v = 0.f;
+    const float* src = p.norm_v + (long long)hk * p.n_tok + first;
+    #pragma unroll 4
+    for (int i = tid; i < len; i += kRangeThreads) v = fmaxf(v, src[i]);
+    for (int h = hk * p.group; h < (hk + 1) * p.group; ++h) {
+      src = p.norm_g + (long long)h * p.n_tok + first;
+      #pragma unroll 4
+      for (int i = tid; i < len; i += kRangeThreads) g = fmaxf(g, src[i]);
+    }
+    #pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, d));
+      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+    }
+    if ((tid & 31) == 0) best[tid >> 5] = make_float2(g, v);
+    __syncthreads();
+    if (tid == 0) {
+      #pragma unroll
+      for (int i = 1; i < kRangeThreads / 32; ++i) {
+        g = fmaxf(g, best[i].x);
+        v = fmaxf(v, best[i].y);
+      }
+      p.range[(long long)hk * p.n_tok + first] = make_float2(g, v);
+    }
+    __syncthreads();
   }
 }
 
@@ -145,7 +226,8 @@ struct PromptBwdLayout {
   static constexpr int kNumBars = bD + 1;
   static constexpr int kItems = (kBars + kNumBars * 8 + 15) & ~15;
   static constexpr int kMisc = kItems + kPrItems * 16;
-  static constexpr int kAlloc = kMisc + 16 + 1024;
+  static constexpr int kTops = kMisc + 16;                 // float[kPrItems]
+  static constexpr int kAlloc = kTops + kPrItems * 4 + 1024;
   static_assert(kAlloc <= 232448, "shared memory");
 };
 
@@ -171,7 +253,8 @@ __device__ __forceinline__ void split3(float v, uint32_t* ab, uint32_t* c) {
   *c = E::pack(v / c2, 0.f) & 0xffffu;
 }
 
-// An item as the ring carries it: {the sequence's first token, its length (0: end of the list), X tile, head}.
+// An item as the ring carries it: {the sequence's first token, its length (0: end of the list), X tile, head}; fp16: and beside it
+// the largest norm of v's rows (q) or the power of two in dS (kv).
 template <typename E, int D, bool kKv>
 __global__ void __launch_bounds__(kPrThreads, 1)
 clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_x2,
@@ -179,10 +262,12 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
                             const __grid_constant__ SeqBwdParams p) {
   using L = PromptBwdLayout<D, kKv>;
   using T = typename E::type;
+  constexpr bool kF16 = !std::is_same<E, Bf16>::value;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
   int4* items = reinterpret_cast<int4*>(smem + L::kItems);
+  float* tops = reinterpret_cast<float*>(smem + L::kTops);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -223,16 +308,19 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
     *reinterpret_cast<uint4*>(smem + L::kOnes + which * 2048 + r * 16) = w;
     fence_proxy_async_smem();
   }
+  if (kF16 && !kKv) asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
   uint32_t n_item = 0;
+  float item_top = 0.f;
   const auto next_item = [&](int4* it, int site) -> bool {
     const uint32_t s = n_item % kPrItems;
     if (!warp_wait(&bars[L::bItemFull + s], (n_item / kPrItems) & 1, abort_flag, kDevTimeoutOther, site, (int)n_item)) return false;
     *it = items[s];
+    if (kF16) item_top = tops[s];
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[L::bItemEmpty + s]);
     ++n_item;
@@ -410,12 +498,17 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
       const long long x = deal(r, blockIdx.x, gridDim.x);
       int4 it = make_int4(0, 0, 0, 0);
       const bool more = x < total;
+      float top = 0.f;
       if (more) {
         int lv;  // steps: level + 1 query tiles (kv: those from the key tile on) or key tiles (q)
         const int s = list.find(x / heads, &lv);
         int first, len;
         seq_range(p.seq_start, p.n_tok, s, &first, &len);
         it = make_int4(first, len, kKv ? ((len + 127) >> 7) - 1 - lv : lv, (int)(x % heads));
+        if (kF16) {
+          const float2 norms = p.range[(long long)(kKv ? it.w / p.parts : it.w / p.group) * p.n_tok + first];
+          top = kKv ? (float)lift_of(norms.x, norms.y) : norms.y;
+        }
       } else if ((long long)r * gridDim.x < total) {
         continue;
       }
@@ -423,6 +516,7 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
       if (!warp_wait(&bars[L::bItemEmpty + s], ((n / kPrItems) & 1) ^ 1, abort_flag, kDevTimeoutOther, 3, (int)n)) break;
       if (lane == 0) {
         items[s] = it;
+        if (kF16) tops[s] = top;
         mbar_arrive(&bars[L::bItemFull + s]);
       }
       __syncwarp();
@@ -434,6 +528,7 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
     regs_dec<kPrRegsLow>();
     if constexpr (kKv) {
       const float root = 1.f / p.scale;  // sqrt(d)
+      const float lift = kF16 ? kBwdLift * 0.69314718055994530942f * root : 0.f;
       int4 it;
       uint32_t slot = 0;
       bool ok = true;
@@ -451,7 +546,7 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
           #pragma unroll
           for (int e = 0; e < 2; ++e) {
             uint32_t l01, l2, d01, d2;
-            split3<E>(v[e].x * root, &l01, &l2);
+            split3<E>(kF16 ? fmaf(v[e].x, root, lift) : v[e].x * root, &l01, &l2);
             split3<E>(v[e].y, &d01, &d2);
             *reinterpret_cast<uint4*>(smem + L::kAug + s * 1024 + (e * 32 + lane) * 16) =
                 make_uint4(l01, l2 | (d01 << 16), (d01 >> 16) | (d2 << 16), 0);
@@ -480,10 +575,14 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
       const bool valid = it.z * 128 + row < it.y;
       const long long tok = (long long)it.x + it.z * 128 + row;
       float2 mine = make_float2(0.f, 0.f);
+      int lift = 0;  // fp16: the power of two in dS: of this row, or (kv) of the sequence and kv head
       if (!kKv && valid) {
         mine = p.stats[(long long)it.w * p.n_tok + tok];
         mine.x *= 1.4426950408889634f;
       }
+      if (kF16) lift = kKv ? (int)item_top : lift_of(valid ? p.norm_g[(long long)it.w * p.n_tok + tok] : 0.f, item_top);
+      const float more = kF16 && kKv ? pow2(lift - (int)kBwdLift) : 1.f;  // P has its own
+      const uint64_t more2 = f32x2_pack(more, more);
       for (int i = 0; i < steps; ++i, ++slot) {
         const uint32_t buf = (2 * i + half) % L::kBufs;
         const int yt = kKv ? it.z + i % per : i;
@@ -537,6 +636,7 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
           mine.y = -(sums[row] + sums[128 + row]);
           if (half == 0 && valid) p.stats[(long long)it.w * p.n_tok + tok].y = mine.y;
         }
+        if (!kKv && kF16 && i == 0) mine.x += (float)lift;  // from here on P, which only dS needs, has its factor
         const auto tile = [&](auto cut) {
           #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -551,7 +651,9 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
               const uint64_t g2 = f32x2_pack(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1]));
               const uint64_t x = kKv ? f32x2_mul(s2, sc2) : f32x2_fma(s2, sc2, f32x2_pack(mine.x, mine.x));
               float p0 = ex2_approx(f32x2_lo(x)), p1 = ex2_approx(f32x2_hi(x));
-              const uint64_t ds = f32x2_mul(f32x2_pack(p0, p1), kKv ? g2 : f32x2_add(g2, f32x2_pack(mine.y, mine.y)));
+              uint64_t pp = f32x2_pack(p0, p1);
+              if (kF16 && kKv) pp = f32x2_mul(pp, more2);
+              const uint64_t ds = f32x2_mul(pp, kKv ? g2 : f32x2_add(g2, f32x2_pack(mine.y, mine.y)));
               float d0 = f32x2_lo(ds), d1 = f32x2_hi(ds);
               if constexpr (decltype(cut)::value) {
                 const int col = c * 32 + 2 * e;
@@ -583,7 +685,8 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
         const SeqView& out = one ? p.out1 : p.out2;
         const int c0 = kKv ? 0 : half * (D / 2);
         const uint32_t acc = tmem + lane_base + (one ? L::kAcc1 : L::kAcc2) + c0;
-        const float f = one ? 1.f : p.scale;
+        const float drop = !kF16 ? 1.f : pow2(-(one ? (int)kBwdLift : lift));
+        const float f = one ? drop : p.scale * drop;
         const bool sums = kKv && p.parts > 1;
         const int hk = kKv ? it.w / p.parts : it.w;
         T* dst = static_cast<T*>(out.ptr) + hk * out.sh + tok * out.st + c0;
@@ -594,6 +697,10 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
           tmem_ld32(acc + c * 32, ov);
           tmem_wait_ld(ov);
           if (valid && sums) {
+            if (kF16) {
+              #pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * drop);
+            }
             #pragma unroll
             for (int e = 0; e < 8; ++e)
               reinterpret_cast<uint4*>(part)[c * 8 + e] = make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);

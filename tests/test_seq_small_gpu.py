@@ -52,7 +52,8 @@ def test_prompt(gap, d, heads):
 @pytest.mark.parametrize("gap", GAPS)
 @pytest.mark.parametrize("dtype,cache", [(torch.float16, None), (torch.float16, "e4m3"), (torch.bfloat16, "e4m3")])
 def test_decode(gap, dtype, cache):
-    n, d, page = 8191, 64, 16
+    # 640 sequences that share their pages: a block has whole ones, so one warp meets the strong key and a quarter of the others.
+    n, d, page, many = 2047, 64, 16, 640
     gen = torch.Generator().manual_seed(2)
     kind = torch.float8_e4m3fn if cache else dtype
     q, k, v = weak(gen, n, d, torch.float16)
@@ -67,8 +68,94 @@ def test_decode(gap, dtype, cache):
         y[order] = rows.view(pages, page, 1, d).to(kind)
     scales = [torch.tensor([gap / 16.0 if cache else 1.0]), torch.tensor([1.0])]
     kw = {"k_scale": scales[0].cuda(), "v_scale": scales[1].cuda()} if cache else {}
-    o, lse = L.clear_attn_decode(q.cuda(), kp.cuda(), vp.cuda(), order[None].to(torch.int32).cuda(), torch.tensor([n], dtype=torch.int32).cuda(), **kw)
+    table = order.to(torch.int32).expand(many, -1).contiguous().cuda()
+    o, lse = L.clear_attn_decode(q.expand(1, many, d).contiguous().cuda(), kp.cuda(), vp.cuda(), table, torch.full((many,), n, dtype=torch.int32).cuda(), **kw)
     assert L.clear_attn_check() == 0
     kc, vc = (x.float()[order].flatten(0, 1)[:n, 0].double() * s.double() for x, s in ((kp, scales[0]), (vp, scales[1])))
-    check("decode", o[0], lse[0], q[0], kc, vc, dtype)
-    assert not math.isnan(float(o.float().sum()))
+    for s in (0, 1, 333, many - 1):
+        check(f"sequence {s}", o[0, s:s + 1], lse[0, s:s + 1], q[0], kc, vc, dtype)
+
+
+def gradients(q, k, v, g, lens):
+    o, lse = L.clear_attn_prompt_fwd(q.cuda(), k.cuda(), v.cuda(), U.starts(lens).cuda())
+    got = L.clear_attn_prompt_bwd(q.cuda(), k.cuda(), v.cuda(), o, lse, g.cuda(), U.starts(lens).cuda())
+    assert L.clear_attn_check() == 0
+    return [x.cpu() for x in got]
+
+
+def check_gradients(got, q, k, v, g, at=0):
+    """One kv head and its group of query heads, one sequence."""
+    n, d = k.shape[1:]
+    t = slice(at, at + n)
+    keep = torch.ones(n, n, dtype=torch.bool).tril()
+    dk = dv = tk = tv = 0
+    for h in range(q.shape[0]):
+        (rq, rk, rv), (eq, ek, ev) = U.gradients(q[h], k[0], v[0], g[h])
+        # D reaches the key gradients as three 16-bit parts, to 2^-38: at most 2^-37 of each P
+        p = torch.exp((q[h].double() @ k[0].double().T / math.sqrt(d)).masked_fill(~keep, -math.inf) -
+                      U.attend(q[h], k[0], v[0], keep)[1][:, None])
+        ek = ek + 2.0 ** -37 / math.sqrt(d) * (p.T @ q[h].double().abs())
+        U.check(f"head {h} dq", got[0][h, t], rq, eq + U.unit(q.dtype) * rq.abs() + U.tiny(q.dtype))
+        dk, dv, tk, tv = dk + rk, dv + rv, tk + ek, tv + ev
+    U.check("dk", got[1][0, t], dk, tk + U.unit(q.dtype) * dk.abs() + U.tiny(q.dtype))
+    U.check("dv", got[2][0, t], dv, tv + U.unit(q.dtype) * dv.abs() + U.tiny(q.dtype))
+
+
+@pytest.mark.parametrize("d,group", [(64, 1), (64, 3), (128, 16)])
+@pytest.mark.parametrize("which", ["dq", "dk"])
+def test_small_upstream_gradients(which, d, group):
+    # dS is about 2^-25 here, a step of fp16 in all; the other factor of dq or dk is large, so that the result is not.
+    gen = torch.Generator().manual_seed(10)
+    n = 600
+    q, k, v, g = (U.packed(gen, h, n, d, torch.float16) for h in (group, 1, 1, group))
+    q, k = (q / 1024, k * 64) if which == "dq" else (q * 64, k / 1024)
+    g = (g.float() * 2.0 ** -20).half()
+    check_gradients(gradients(q, k, v, g, [n]), q, k, v, g)
+
+
+@pytest.mark.parametrize("gap", GAPS)
+def test_gradients_of_weak_keys(gap):
+    n, d = 2048, 64
+    gen = torch.Generator().manual_seed(11)
+    q, k, v = weak(gen, n, d, torch.float16)
+    k[0, 0, 0] = gap
+    g = (1 + torch.rand(1, n, d, generator=gen)).half()
+    check_gradients(gradients(q, k, v, g, [n]), q, k, v, g)
+
+
+@pytest.mark.parametrize("d,group", [(64, 1), (128, 4)])
+def test_large_upstream_gradients(d, group):
+    # dP is about 4e5, out of fp16's range; dq, dk and dv are in it.
+    gen = torch.Generator().manual_seed(12)
+    n = 300
+    q, k, v, g = (U.packed(gen, h, n, d, torch.float16) for h in (group, 1, 1, group))
+    q, k, v, g = q / 4096, k / 4096, v * 200, g * 200
+    check_gradients(gradients(q, k, v, g, [n]), q, k, v, g)
+
+
+def test_sequences_of_unlike_size():
+    gen = torch.Generator().manual_seed(13)
+    lens, d = [200, 140, 300], 128
+    q, k, v, g = (U.packed(gen, h, sum(lens), d, torch.float16) for h in (2, 1, 1, 2))
+    g[:, :200] *= 100
+    g[:, 200:340] *= 1e-4
+    got = gradients(q, k, v, g, lens)
+    for at, n in ((0, 200), (200, 140), (340, 300)):
+        t = slice(at, at + n)
+        check_gradients(got, q[:, t], k[:, t], v[:, t], g[:, t], at)
+    for x in (q, k, v, g):  # what one of them holds is nothing to the others
+        x[:, 200:340] = math.inf
+    v[:, 250] = math.nan
+    again = gradients(q, k, v, g, lens)
+    for t in (slice(0, 200), slice(340, 640)):
+        assert all(torch.equal(a[:, t], b[:, t]) for a, b in zip(got, again))
+
+
+def test_zero_gradients_and_rows():
+    gen = torch.Generator().manual_seed(14)
+    q, k, v, g = (U.packed(gen, h, 200, 64, torch.float16) for h in (2, 1, 1, 2))
+    assert all((x == 0).all() for x in gradients(q, k, v, torch.zeros_like(g), [200])[:2])
+    g[:, ::3] = 0
+    check_gradients(gradients(q, k, v, g, [200]), q, k, v, g)
+    v[:] = 0
+    check_gradients(gradients(q, k, v, g, [200]), q, k, v, g)
