@@ -30,7 +30,8 @@
 // shared memory, against the products' operands, they took 800 of 2000 cycles a half. They ride along in the
 // products instead: one more step of 16 along the reduced axis, X = constants, Y = -lse sqrt(d) and -D as
 // three parts each of 16-bit type, whose products with the constants add up to the fp32 value (24 bits
-// and more). P = 2^(S' log2 e / sqrt(d)) and dS = P dP' then need no other input.
+// and more). P = 2^(S' log2 e / sqrt(d)) and dS = P dP' then need no other input. (What the parts cannot hold, lse of a
+// million and more in fp16, is added to their columns by the softmax warpgroups.)
 //
 // P and dS are rounded to the element type; sums, statistics and accumulators are fp32. In bf16 that is half a step of each, 2^-8
 // at most. fp16's steps are absolute below 2^-14, where P (about 1 / keys) and dS = P (dP - D) of small gradients lie, and its
@@ -227,7 +228,8 @@ struct PromptBwdLayout {
   static constexpr int kItems = (kBars + kNumBars * 8 + 15) & ~15;
   static constexpr int kMisc = kItems + kPrItems * 16;
   static constexpr int kTops = kMisc + 16;                 // float[kPrItems]
-  static constexpr int kAlloc = kTops + kPrItems * 4 + 1024;
+  static constexpr int kFar = kTops + kPrItems * 4;        // int[kStages]: fp16: whether a half has rows that are far
+  static constexpr int kAlloc = kFar + kStages * 4 + 1024;
   static_assert(kAlloc <= 232448, "shared memory");
 };
 
@@ -236,13 +238,18 @@ __device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t k_s
   return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((k_step >> 4) & 0x3FFFu) << 16) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1u << 46);
 }
 
+// Statistics that do not fit their three parts in fp16: such a row's are added to its column by the threads that use it. -inf, the
+// statistics of a row without a finite score, does: P is 0.
+constexpr float kFarLimit = 8e6f;
+__device__ __forceinline__ bool is_far(float x, float d) { return (fabsf(x) > kFarLimit && x != -INFINITY) || fabsf(d) > kFarLimit; }
+
 // v as three 16-bit parts: v = c0 a + c1 b + c2 c with the constants below. bf16 has fp32's range: the constants
 // are 1, each part takes 8 bits. fp16 takes 11 bits each; its constants (2^7, 2^-3, 2^-13) reach from 8e6 down to steps of
-// 2^-37. Larger values are cut to the limit (P is 0 then, or the gradient out of fp16's range).
+// 2^-37. -inf is cut to the limit.
 template <typename E>
 __device__ __forceinline__ void split3(float v, uint32_t* ab, uint32_t* c) {
   constexpr bool kB = std::is_same<E, Bf16>::value;
-  constexpr float kLimit = kB ? 1e30f : 8e6f;
+  constexpr float kLimit = kB ? 3e38f : kFarLimit;
   constexpr float c0 = kB ? 1.f : 128.f, c1 = kB ? 1.f : 0.125f, c2 = kB ? 1.f : 1.f / 8192.f;
   v = v > kLimit ? kLimit : v < -kLimit ? -kLimit : v;
   const uint32_t w0 = E::pack(v / c0, 0.f);
@@ -251,6 +258,37 @@ __device__ __forceinline__ void split3(float v, uint32_t* ab, uint32_t* c) {
   v = fmaf(-c1, E::lo(w1), v);
   *ab = (w0 & 0xffffu) | (w1 << 16);
   *c = E::pack(v / c2, 0.f) & 0xffffu;
+}
+
+// A streamed row's -lse as it is added to its column of S: times sqrt(d), and in fp16 with P's power of two.
+template <typename E>
+__device__ __forceinline__ float shift_of(float neg_lse, float root) {
+  return std::is_same<E, Bf16>::value ? neg_lse * root : fmaf(neg_lse, root, kBwdLift * 0.69314718055994530942f * root);
+}
+
+// fp16: adds to a half's 64 columns of S and dP, in this warp's lanes, the statistics of the rows that are far, `left` of the rows
+// being the sequence's. Whole warp; rare, and not inlined: it would cost the loop around it registers.
+__device__ __noinline__ void add_far(uint32_t s_tm, const float2* stats, int left, float root) {
+  #pragma unroll 1
+  for (int c = 0; c < 64; c += 32) {
+    uint32_t s[32], g[32];
+    tmem_ld32(s_tm + c, s);
+    tmem_ld32(s_tm + 64 + c, g);
+    tmem_wait_ld(s);
+    tmem_wait_ld(g);
+    #pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float2 w = c + e < left ? stats[c + e] : make_float2(0.f, 0.f);
+      const float x = shift_of<Fp16>(w.x, root);
+      if (is_far(x, w.y)) {
+        s[e] = __float_as_uint(__uint_as_float(s[e]) + x);
+        g[e] = __float_as_uint(__uint_as_float(g[e]) + w.y);
+      }
+    }
+    tmem_st32(s_tm + c, s);
+    tmem_st32(s_tm + 64 + c, g);
+  }
+  tmem_wait_st();
 }
 
 // An item as the ring carries it: {the sequence's first token, its length (0: end of the list), X tile, head}; fp16: and beside it
@@ -268,6 +306,7 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
   int4* items = reinterpret_cast<int4*>(smem + L::kItems);
   float* tops = reinterpret_cast<float*>(smem + L::kTops);
+  int* far = reinterpret_cast<int*>(smem + L::kFar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -338,6 +377,7 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
     const int part = it.w % p.parts;
     return (part + 1) * p.group / p.parts - part * p.group / p.parts;
   };
+  const float root = 1.f / p.scale;  // sqrt(d)
   const auto steps_of = [&](const int4& it) { return kKv ? h_count(it) * (n_tiles(it) - it.z) : it.z + 1; };
 
   if (warp == 8) {
@@ -527,8 +567,6 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
     // ------------------------------------------------------------------ statistics of streamed rows
     regs_dec<kPrRegsLow>();
     if constexpr (kKv) {
-      const float root = 1.f / p.scale;  // sqrt(d)
-      const float lift = kF16 ? kBwdLift * 0.69314718055994530942f * root : 0.f;
       int4 it;
       uint32_t slot = 0;
       bool ok = true;
@@ -543,13 +581,23 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
           const uint32_t s = slot % L::kStages;
           ok = warp_wait(&bars[L::bYEmpty + s], ((slot / L::kStages) & 1) ^ 1, abort_flag, kDevTimeoutOther, 4, (int)slot);
           if (!ok) break;
+          bool any = false;
           #pragma unroll
           for (int e = 0; e < 2; ++e) {
             uint32_t l01, l2, d01, d2;
-            split3<E>(kF16 ? fmaf(v[e].x, root, lift) : v[e].x * root, &l01, &l2);
-            split3<E>(v[e].y, &d01, &d2);
+            float x = shift_of<E>(v[e].x, root), d = v[e].y;
+            if (kF16 && is_far(x, d)) {
+              any = true;
+              x = d = 0.f;
+            }
+            split3<E>(x, &l01, &l2);
+            split3<E>(d, &d01, &d2);
             *reinterpret_cast<uint4*>(smem + L::kAug + s * 1024 + (e * 32 + lane) * 16) =
                 make_uint4(l01, l2 | (d01 << 16), (d01 >> 16) | (d2 << 16), 0);
+          }
+          if (kF16) {
+            any = __any_sync(0xffffffffu, any);
+            if (lane == 0) far[s] = any;
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -613,6 +661,10 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
             for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(y + (c >> 3) * L::kYBlock + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
+        }
+        if (kF16 && kKv && far[st]) {
+          const int t0 = yt * 128 + half * 64;
+          add_far(s_tm, p.stats + (long long)(h_first(it) + i / per) * p.n_tok + it.x + t0, it.y - t0, root);
         }
         const bool all = lo <= 0 && hi >= 64;
         const bool warp_all = __all_sync(0xffffffffu, all);

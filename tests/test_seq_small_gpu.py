@@ -159,3 +159,43 @@ def test_zero_gradients_and_rows():
     check_gradients(gradients(q, k, v, g, [200]), q, k, v, g)
     v[:] = 0
     check_gradients(gradients(q, k, v, g, [200]), q, k, v, g)
+
+
+def test_gradients_of_far_scores():
+    # Scores of a million: each key is its own query's only one. q k is exact (multiples of 90000 under 2^24); its
+    # logarithm to base 2 in fp32 has steps of 1/8, and lse, a natural one, of 1/16. The forward rounds to them twice
+    # (2 * 1/16 in base 2) and lse once, the gradients lse sqrt(d) (steps of 1: 0.5 / sqrt(d)) or lse log2 e (1/16 in base 2), and the scale's
+    # own rounding (2^-24 of a million: 0.06) does not cancel between base 2 and lse: P = 1 is off by e^0.3 at most.
+    n, d = 300, 128
+    gen = torch.Generator().manual_seed(15)
+    q = (300.0 * (torch.randint(0, 2, (1, n, d), generator=gen) * 2 - 1)).half()
+    q[:, 100:200] /= 16  # and rows with ordinary statistics between them
+    v, g = (U.packed(gen, 1, n, d, torch.float16) for _ in range(2))
+    dq, dk, dv = (x[0].double() for x in gradients(q, q, v, g, [n]))
+    own = torch.ones(n, dtype=torch.bool)
+    own[100:200] = False  # their own key is not their largest: another's is
+    x = (q[0].double() @ q[0].double().T / math.sqrt(d)).masked_fill(~torch.ones(n, n, dtype=torch.bool).tril(), -math.inf)
+    p = torch.softmax(x, -1)
+    assert (p[own].amax(-1) == 1).all() and (p[own].argmax(-1) == torch.arange(n)[own]).all()
+    off = math.exp(0.3) - 1
+    ref, size = p.T @ g[0].double(), p.T @ g[0].double().abs()
+    U.check("dv", dv, ref, off * size + 2.0 ** -9 * size + U.tiny(torch.float16))
+    # dP and D are equal up to o's rounding: dq and dk are no more than that leaves
+    left = math.exp(0.3) * (g[0].double().abs() * v[0].double().abs()).sum(-1) * 2.0 ** -10
+    scale = 300 / math.sqrt(d)
+    far = own & (torch.arange(n) >= 128)
+    assert (dq[far].abs() <= (left * scale)[far][:, None]).all()
+    assert not dk.isnan().any() and not dk.isinf().any()
+    later = torch.arange(n) >= 200  # keys that only their own rows read
+    assert (dk[later].abs() <= (left * scale)[later][:, None]).all()
+
+
+@pytest.mark.parametrize("d,group", [(64, 2), (128, 1)])
+def test_gradients_of_far_sums(d, group):
+    # D = dO o is about 4e7 in the first rows, and less further on.
+    gen = torch.Generator().manual_seed(16)
+    n = 260
+    q, k, v, g = (U.packed(gen, h, n, d, torch.float16) for h in (group, 1, 1, group))
+    q, k, v, g = q / 8192, k / 8192, v * 4000, g * 1000
+    assert (g[0].double() * v[0].double()).sum(-1)[0].abs() > 8e6 or d == 64
+    check_gradients(gradients(q, k, v, g, [n]), q, k, v, g)
