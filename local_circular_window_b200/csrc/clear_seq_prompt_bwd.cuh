@@ -44,8 +44,9 @@
 //
 // D from the given o carries o's rounding, which dS = P (dP - D) shares along the whole row: against the
 // rounding of dS itself that is about one part in sqrt(keys), so it shows only in a sequence's first
-// rows. The q kernel takes D = sum P dP there instead: the first query tile has one key tile, so a
-// row's sum is at hand (the two halves exchange theirs). It leaves that D for the kv kernel.
+// rows. The q kernel takes D = sum P dP / sum P there instead: the first query tile has one key tile, so a
+// row's sums are at hand (the two halves exchange theirs). sum P is 1 but for what lse's own rounding leaves: of scores of a
+// million, whose lse has steps of 1/16, it may be 0.9, and D must follow. It leaves that D for the kv kernel.
 // Error of dq at 2000 rows of d = 64 in fp16, relative to the result's own rounding: 1.55 before, 1.44 after.
 //
 // Bound by the tensor cores: a 128 x 128 pair of tiles costs 4 (kv) or 3 (q) products of 512 cycles at
@@ -668,24 +669,31 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
         }
         const bool all = lo <= 0 && hi >= 64;
         const bool warp_all = __all_sync(0xffffffffu, all);
-        if (!kKv && it.z == 0) {  // a sequence's first rows: D = sum P dP over the only key tile
-          float sum = 0.f;
+        if (!kKv && it.z == 0) {  // a sequence's first rows: D = sum P dP / sum P over the only key tile
+          float sum = 0.f, all_p = 0.f;
           #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t s[32], g[32];
             tmem_ld32(s_tm + c * 32, s);
             tmem_ld32(d_tm + c * 32, g);
-            tmem_wait_ld();
+            tmem_wait_ld(s);
+            tmem_wait_ld(g);
             #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (c * 32 + e < hi) sum = fmaf(ex2_approx(fmaf(__uint_as_float(s[e]), p.scale_log2, mine.x)), __uint_as_float(g[e]), sum);
+              if (c * 32 + e < hi) {
+                const float pe = ex2_approx(fmaf(__uint_as_float(s[e]), p.scale_log2, mine.x));
+                all_p += pe;
+                sum = fmaf(pe, __uint_as_float(g[e]), sum);
+              }
           }
-          float* sums = reinterpret_cast<float*>(smem + L::kAug);
-          sums[half * 128 + row] = sum;
+          float2* sums = reinterpret_cast<float2*>(smem + L::kAug);
+          sums[half * 128 + row] = make_float2(sum, all_p);
           mbar_arrive(&bars[L::bD]);
           if (!warp_wait(&bars[L::bD], nd_phase & 1, abort_flag, kDevTimeoutSoftmax, 26 + half, (int)nd_phase)) goto done;
           ++nd_phase;
-          mine.y = -(sums[row] + sums[128 + row]);
+          const float2 u = sums[row], w = sums[128 + row];
+          all_p = u.y + w.y;
+          mine.y = all_p == 0.f ? 0.f : -(u.x + w.x) / all_p;
           if (half == 0 && valid) p.stats[(long long)it.w * p.n_tok + tok].y = mine.y;
         }
         if (!kKv && kF16 && i == 0) mine.x += (float)lift;  // from here on P, which only dS needs, has its factor
