@@ -501,8 +501,9 @@ CLEAR_API clear_status_t clear_attn_prompt_fwd(const clear_seq_params_t* params,
                                                const clear_seq_view_t* v, const clear_seq_view_t* o, float* lse,
                                                void* stream);
 
-/* Workspace bytes of clear_attn_prompt_bwd (of either type): three fp32 per row and query head, three per row and key/value head
- * and, where few key/value heads leave the GPU idle, fp32 partial sums of dk and dv (at most about 77 MB). */
+/* Workspace bytes of clear_attn_prompt_bwd (of either type): three fp32 per row and query head, three per row and key/value
+ * head and, where few key/value heads leave the GPU idle, fp32 partial sums of dk and dv (at most about 77 MB). They hold for
+ * every smaller n_tok with the same heads and d, and do not depend on n_seq. */
 CLEAR_API size_t clear_attn_prompt_bwd_workspace_size(const clear_seq_params_t* params, clear_status_t* status);
 
 /*

@@ -233,6 +233,18 @@ PromptBwdWorkspace prompt_bwd_workspace_layout(const clear_seq_params_t* p) {
   return w;
 }
 
+// What n_tok tokens and any smaller number need at most: fewer tokens may take more parts. The parts change only with the number
+// of 128-token tiles, and between two changes more tokens need more.
+size_t prompt_bwd_workspace_most(const clear_seq_params_t* p) {
+  clear_seq_params_t x = *p;
+  size_t most = prompt_bwd_workspace_layout(p).total;
+  for (x.n_tok = 128; x.n_tok < p->n_tok && bwd_parts(&x) > 1; x.n_tok += 128) {
+    const size_t total = prompt_bwd_workspace_layout(&x).total;
+    if (total > most) most = total;
+  }
+  return most;
+}
+
 constexpr int kRangeBlocks = 1024;  // along the sequences
 
 template <typename E, int D>
@@ -403,7 +415,7 @@ clear_status_t clear_attn_prompt_fwd(const clear_seq_params_t* params, const int
 size_t clear_attn_prompt_bwd_workspace_size(const clear_seq_params_t* params, clear_status_t* status) {
   const clear_status_t st = check_seq_params(params);
   if (status) *status = st;
-  return st == CLEAR_OK ? prompt_bwd_workspace_layout(params).total : 0;
+  return st == CLEAR_OK ? prompt_bwd_workspace_most(params) : 0;
 }
 
 clear_status_t clear_attn_prompt_bwd(const clear_seq_params_t* params, const int* seq_start, const clear_seq_view_t* q,
