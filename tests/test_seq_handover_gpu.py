@@ -5,6 +5,7 @@ import torch
 
 import local_circular_window_b200 as L
 import seq_util as U
+import test_seq_prompt_bwd_gpu as B
 from test_seq_prompt_gpu import make, verify
 
 pytestmark = pytest.mark.gpu
@@ -62,3 +63,33 @@ def test_split_items_that_end_in_one_tile(d, heads):
     assert sum(lens) >= 512 * len(lens)
     o, lse = forward(q, k, v, ss)
     verify(o, lse, q, k, v, lens, heads=[0, heads - 1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("hq,hk", [(32, 16), (32, 2)], ids=["whole-groups", "parts"])
+def test_gradients(hq, hk, dtype):
+    # 1024 items of query tiles, and 512 of key tiles, or 384 where groups are split into six parts.
+    q, k, v, g, ss = B.make(53, LENS, hq, hk, 128, dtype)
+    got = B.both(q, k, v, g, ss)
+    assert L.clear_attn_check() == 0
+    B.verify(got, q, k, v, g, LENS, kv_heads=[hk - 1] if hk == 2 else [0, 7, 15])
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(got, B.both(q, k, v, g, ss)))
+
+
+def test_captured_step_in_fp16():
+    # All of a training step's kernels, programmatic dependents among them, in a graph that is replayed with other data.
+    q, k, v, g, ss = (x.cuda() for x in B.make(54, [300, 200, 100], 6, 2, 128, torch.float16))
+    ws = torch.empty(L.prompt_bwd_workspace_size(600, 6, 2, 128), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = L.clear_attn_prompt_fwd(q, k, v, ss)
+        got = L.clear_attn_prompt_bwd(q, k, v, o, lse, g, ss, workspace=ws)
+    for i, offsets in enumerate([[0, 10, 10, 600], [0, 599, 600, 600], [0, 200, 400, 600]]):
+        ss.copy_(torch.tensor(offsets, dtype=torch.int32))
+        g *= 2.0 ** -i
+        v *= 2.0
+        want = B.both(q, k, v, g, ss)
+        ws.fill_(0xFF)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
