@@ -1,11 +1,12 @@
 """The barriers of the causal prompt forward, gone through on the CPU.
 
-A model of one block: the issuing thread, a tensor pipe that completes products in the order of issue, and the two softmax
-warpgroups as warps of their own, with barriers that are waited for by parity as the hardware's are (a wait passes when the
-barrier's current phase has the other parity, be it one phase further or one phase behind). The order of the
-products and the waits that follow from it are the kernel's own, from csrc/clear_seq_order.h. Random
+A model of one block: the loader, copies that land in any order, the issuing thread, a tensor pipe that completes products in the order
+of issue, and the two softmax warpgroups as warps of their own, with barriers that are waited for by parity as the hardware's
+are (a wait passes when the barrier's current phase has the other parity, be it one phase further or one phase behind). The
+order of the products and the waits that follow from it are the kernel's own, from csrc/clear_seq_order.h. Random
 schedules, with agents that stall for long, look for a wait that passes before its phase is complete, for an
-accumulator that is read before its last product, and for a half's sums that are read after they were replaced.
+accumulator that is read before its last product, for a half's sums that are read after they were replaced, and for tiles in the ring
+that are not the ones meant.
 """
 import ctypes
 import os
@@ -66,9 +67,59 @@ class Block:
         self.p = {(b, i): Bar(WARPS) for b in range(bufs) for i in (0, 1)}
         self.o = [Bar(1), Bar(1)]
         self.join, self.joined = Bar(2 * WARPS), Bar(2 * WARPS)
-        self.pipe = []
+        self.pipe, self.flying = [], []
+        self.stages = {2: 5, 3: 8}[bufs]
+        self.full, self.empty = ([Bar(1) for _ in range(self.stages)] for _ in range(2))
+        self.q_full, self.q_empty = Bar(1), Bar(1)
+        self.ring = [None] * self.stages
         self.ml = {}
         self.acc = [[], []]   # key tiles whose P V has been added to each accumulator, (item, tile)
+
+    def key_tile(self, half, i):
+        return 2 * i + half if self.split else i
+
+    def place(self, n, what, j):
+        """Place in the ring of a tile of item n: K0 K1 V0 K2 V1 ... V(last), behind those of earlier items."""
+        tiles = [t + 1 if two and not self.split else t for t, two in self.items]
+        m = tiles[n]
+        at = (0 if j == 0 else 2 * j - 1) if what == "K" else (2 * m - 1 if j == m - 1 else 2 * j + 2)
+        return 2 * sum(tiles[:n]) + at
+
+    def loader(self):
+        at = 0
+        for n, (t, two) in enumerate(self.items):
+            m = t + 1 if two and not self.split else t
+            yield from self.wait("Q empty", self.q_empty, n - 1)
+            self.flying.append((self.q_full, None, None))
+            for j in range(m + 1):
+                for what, x in (("K", j), ("V", j - 1)):
+                    if not 0 <= x < m:
+                        continue
+                    s = at % self.stages
+                    assert self.place(n, what, x) == at
+                    yield from self.wait("ring empty", self.empty[s], at // self.stages - 1)
+                    self.ring[s] = None
+                    self.flying.append((self.full[s], s, (n, what, x)))
+                    at += 1
+                    yield
+
+    def copies(self):
+        while True:
+            if self.flying:
+                bar, s, tile = self.flying.pop(int(self.rng.random() * len(self.flying)))
+                if s is not None:
+                    self.ring[s] = tile
+                bar.arrive()
+            yield
+
+    def tile(self, n, what, j):
+        """Waits for a tile of the ring; returns its stage."""
+        at = self.place(n, what, j)
+        s = at % self.stages
+        yield from self.wait(f"ring full, {what}", self.full[s], at // self.stages)
+        if self.ring[s] != (n, what, j):
+            raise Fault(f"{(n, what, j)} is not in the ring, but {self.ring[s]}")
+        return s
 
     def counts(self, it):
         tiles, two = it
@@ -76,7 +127,7 @@ class Block:
 
     def wait(self, name, bar, n):
         """Waits for the end of the barrier's phase number n (from 0), by parity."""
-        while bar.phase & 1 == n & 1:
+        while bar.phase & 1 == n & 1:  # n = -1: the phase before the first, which counts as complete
             yield
         if bar.phase < n + 1:
             raise Fault(f"{name}: a wait for phase {n} passed in phase {bar.phase}")
@@ -91,25 +142,43 @@ class Block:
             alone = self.order(1, it)
             ahead = 0
 
+            users = {}  # products still to come for each tile in the ring
+            for h, i in places.values():
+                for what in "KV":
+                    users[what, self.key_tile(h, i)] = users.get((what, self.key_tile(h, i)), 0) + 1
+
+            def used(what, j, s):
+                users[what, j] -= 1
+                if users[what, j] == 0:
+                    self.pipe.append(("commit", self.empty[s]))
+
             def issue(b):
                 nonlocal ahead
-                h, _ = places[ahead]
+                h, i = places[ahead]
                 assert b == ahead % self.bufs
+                j = self.key_tile(h, i)
+                s = yield from self.tile(n, "K", j)
                 self.pipe.append(("S", self.s[b, h]))
+                used("K", j, s)
                 ahead += 1
+                if ahead == total:
+                    self.pipe.append(("commit", self.q_empty))
 
+            yield from self.wait("Q", self.q_full, n)
             while ahead < total and self.order(2, it, ahead):
-                issue(ahead % self.bufs)
+                yield from issue(ahead % self.bufs)
             if self.split:
                 yield from self.wait("accumulators", self.joined, n - 1)
             for g in range(total):
                 h, i = places[g]
+                s = yield from self.tile(n, "V", self.key_tile(h, i))
                 for part in (0, 1):
                     yield from self.wait(f"P {part}", self.p[g % self.bufs, part], uses[g % self.bufs])
                 uses[g % self.bufs] += 1
                 self.pipe.append(("PV", self.o[h], h, (n, i)))
+                used("V", self.key_tile(h, i), s)
                 if ahead < total:
-                    issue((g + 1) % self.bufs if alone else g % self.bufs)
+                    yield from issue((g + 1) % self.bufs if alone else g % self.bufs)
                 yield
 
     def tensor(self):
@@ -135,6 +204,9 @@ class Block:
                 yield
                 if i > 0 and self.rng.random() < 0.3:  # the maximum moves: the accumulator is rescaled
                     yield from self.wait(f"P V {half}, rescaling", self.o[half], no + i - 1)
+                diagonal = self.key_tile(half, i) == it[0] - 1 if self.split else i == m - 1 and (half == 1 or not it[1])
+                if diagonal:  # value rows behind the sequence's end are cleared
+                    yield from self.tile(n, "V", self.key_tile(half, i))
                 self.p[b, 0].arrive()
                 yield
                 if self.order(3, it, half, i):
@@ -168,7 +240,7 @@ class Block:
 
     def run(self):
         left = {(h, w) for h in (0, 1) for w in range(WARPS)}
-        agents = {("issuer", 0): self.issuer(), ("tensor", 0): self.tensor()}
+        agents = {("issuer", 0): self.issuer(), ("tensor", 0): self.tensor(), ("loader", 0): self.loader(), ("copies", 0): self.copies()}
         agents |= {x: self.warp(*x, left) for x in left}
         names, stalled = list(agents), {}
         rng, idle = self.rng, 0
@@ -186,7 +258,7 @@ class Block:
 
 
 SHAPES = [[(1, True), (2, True), (4, True)], [(3, False), (1, False), (2, False)], [(3, True), (2, False), (1, True), (1, False)],
-          [(5, False), (1, False), (1, False), (2, False)], [(6, True), (1, True), (1, True)]]
+          [(5, False), (1, False), (1, False), (1, False), (1, False), (2, False)], [(6, True), (1, True), (1, True)]]
 
 
 @pytest.mark.parametrize("bufs", [2, 3])
