@@ -1,4 +1,4 @@
-"""The barriers of the causal prompt forward, gone through on the CPU.
+"""The barriers of the causal prompt forward and of its gradients, gone through on the CPU.
 
 A model of one block: the loader, copies that land in any order, the issuing thread, a tensor pipe that completes products in the order
 of issue, and the two softmax warpgroups as warps of their own, with barriers that are waited for by parity as the hardware's
@@ -6,7 +6,7 @@ are (a wait passes when the barrier's current phase has the other parity, be it 
 order of the products and the waits that follow from it are the kernel's own, from csrc/clear_seq_order.h. Random
 schedules, with agents that stall for long, look for a wait that passes before its phase is complete, for an
 accumulator that is read before its last product, for a half's sums that are read after they were replaced, and for tiles in the ring
-that are not the ones meant.
+that are not the ones meant. The gradients' kernel (its order has no such header) is restated from its code below.
 """
 import ctypes
 import os
@@ -57,21 +57,68 @@ class Bar:
             self.pending, self.phase = self.count, self.phase + 1
 
 
-class Block:
+class Machine:
+    """Agents that take steps in a random order, with stalls; `left` are the ones that have to end."""
+
+    def __init__(self, rng):
+        self.rng, self.pipe, self.flying, self.ring = rng, [], [], {}
+
+    def wait(self, name, bar, n):
+        """Waits for the end of the barrier's phase number n (from 0), by parity."""
+        while bar.phase & 1 == n & 1:  # n = -1: the phase before the first, which counts as complete
+            yield
+        if bar.phase < n + 1:
+            raise Fault(f"{name}: a wait for phase {n} passed in phase {bar.phase}")
+
+    def copies(self):
+        while True:
+            if self.flying:
+                bar, s, tile = self.flying.pop(int(self.rng.random() * len(self.flying)))
+                if s is not None:
+                    self.ring[s] = tile
+                bar.arrive()
+            yield
+
+    def tensor(self):
+        while True:
+            if self.pipe:
+                op = self.pipe.pop(0)
+                if op[0] == "PV":
+                    self.acc[op[2]].append(op[3])
+                if op[1] is not None:
+                    op[1].arrive()
+            yield
+
+    def go(self, agents, left):
+        names, stalled = list(agents), {}
+        rng, idle = self.rng, 0
+        while left:
+            idle += 1
+            assert idle < 200000, "no progress"
+            a = names[int(rng.random() * len(names))]
+            if stalled.get(a, 0) > 0:
+                stalled[a] -= 1
+                continue
+            if rng.random() < 0.04:
+                stalled[a] = int(rng.random() * 60)
+            if a in agents and next(agents[a], "end") == "end":
+                del agents[a]
+
+
+class Block(Machine):
     """items: for each its number of key tiles and whether it has a tile B."""
 
     def __init__(self, order, bufs, split, items, rng):
-        self.bufs, self.split, self.items, self.rng = bufs, split, items, rng
+        super().__init__(rng)
+        self.bufs, self.split, self.items = bufs, split, items
         self.order = lambda what, it, x=0, y=0: order(bufs, int(split), what, *self.counts(it), x, y)
         self.s = {(b, h): Bar(1) for b in range(bufs) for h in (0, 1)}
         self.p = {(b, i): Bar(WARPS) for b in range(bufs) for i in (0, 1)}
         self.o = [Bar(1), Bar(1)]
         self.join, self.joined = Bar(2 * WARPS), Bar(2 * WARPS)
-        self.pipe, self.flying = [], []
         self.stages = {2: 5, 3: 8}[bufs]
         self.full, self.empty = ([Bar(1) for _ in range(self.stages)] for _ in range(2))
         self.q_full, self.q_empty = Bar(1), Bar(1)
-        self.ring = [None] * self.stages
         self.ml = {}
         self.acc = [[], []]   # key tiles whose P V has been added to each accumulator, (item, tile)
 
@@ -103,15 +150,6 @@ class Block:
                     at += 1
                     yield
 
-    def copies(self):
-        while True:
-            if self.flying:
-                bar, s, tile = self.flying.pop(int(self.rng.random() * len(self.flying)))
-                if s is not None:
-                    self.ring[s] = tile
-                bar.arrive()
-            yield
-
     def tile(self, n, what, j):
         """Waits for a tile of the ring; returns its stage."""
         at = self.place(n, what, j)
@@ -124,13 +162,6 @@ class Block:
     def counts(self, it):
         tiles, two = it
         return ((tiles + 1) // 2, tiles // 2) if self.split else (tiles, tiles + 1 if two else 0)
-
-    def wait(self, name, bar, n):
-        """Waits for the end of the barrier's phase number n (from 0), by parity."""
-        while bar.phase & 1 == n & 1:  # n = -1: the phase before the first, which counts as complete
-            yield
-        if bar.phase < n + 1:
-            raise Fault(f"{name}: a wait for phase {n} passed in phase {bar.phase}")
 
     def issuer(self):
         uses = [0] * self.bufs
@@ -180,15 +211,6 @@ class Block:
                 if ahead < total:
                     yield from issue((g + 1) % self.bufs if alone else g % self.bufs)
                 yield
-
-    def tensor(self):
-        while True:
-            if self.pipe:
-                op = self.pipe.pop(0)
-                if op[0] == "PV":
-                    self.acc[op[2]].append(op[3])
-                op[1].arrive()
-            yield
 
     def warp(self, half, w, left):
         no = joins = 0
@@ -242,19 +264,7 @@ class Block:
         left = {(h, w) for h in (0, 1) for w in range(WARPS)}
         agents = {("issuer", 0): self.issuer(), ("tensor", 0): self.tensor(), ("loader", 0): self.loader(), ("copies", 0): self.copies()}
         agents |= {x: self.warp(*x, left) for x in left}
-        names, stalled = list(agents), {}
-        rng, idle = self.rng, 0
-        while left:
-            idle += 1
-            assert idle < 100000, "no progress"
-            a = names[int(rng.random() * len(names))]
-            if stalled.get(a, 0) > 0:
-                stalled[a] -= 1
-                continue
-            if rng.random() < 0.04:
-                stalled[a] = int(rng.random() * 60)
-            if a in agents and next(agents[a], "end") == "end":
-                del agents[a]
+        self.go(agents, left)
 
 
 SHAPES = [[(1, True), (2, True), (4, True)], [(3, False), (1, False), (2, False)], [(3, True), (2, False), (1, True), (1, False)],
@@ -270,3 +280,128 @@ def test_every_wait_sees_its_phase(order, bufs, split):
         if split:
             items = [(n, False) for n, _ in items]
         Block(order, bufs, split, items, rng).run()
+
+
+class Gradients(Machine):
+    """The gradients' kernel. items: steps (pairs of streamed halves) of each; kv: the kernel of dK and dV, else of dQ, whose items of
+    one step exchange the first rows' sums."""
+
+    def __init__(self, bufs, kv, items, rng):
+        super().__init__(rng)
+        self.bufs, self.kv, self.items, self.stages = bufs, kv, items, {2: 4, 3: 8}[bufs]
+        self.x_full, self.x_empty, self.acc_bar, self.acc_free = Bar(1), Bar(1), Bar(1), Bar(2 * WARPS)
+        self.full = [Bar(2 if kv else 1) for _ in range(self.stages)]
+        self.empty = [Bar(1) for _ in range(self.stages)]
+        self.s, self.p = ([Bar(c) for _ in range(bufs)] for c in (1, WARPS))
+        self.d = Bar(2 * WARPS)
+        self.acc = [[]]
+        self.far, self.sums = {}, {}
+
+    def loader(self):
+        at = 0
+        for n, steps in enumerate(self.items):
+            yield from self.wait("X empty", self.x_empty, n - 1)
+            self.flying.append((self.x_full, None, None))
+            for i in range(2 * steps):
+                s = at % self.stages
+                yield from self.wait("Y empty", self.empty[s], at // self.stages - 1)
+                self.ring[s] = None
+                self.flying.append((self.full[s], s, (n, i)))
+                at += 1
+                yield
+
+    def statistics(self):
+        at = 0
+        for n, steps in enumerate(self.items):
+            for i in range(2 * steps):
+                s = at % self.stages
+                yield from self.wait("Y empty, statistics", self.empty[s], at // self.stages - 1)
+                self.far[s] = (n, i)
+                yield
+                self.full[s].arrive()
+                at += 1
+                yield
+
+    def issuer(self):
+        at, uses = 0, [0] * self.bufs
+        for n, steps in enumerate(self.items):
+            halves, ahead, stage = 2 * steps, 0, [0] * self.bufs
+
+            def scores(b):
+                nonlocal at, ahead
+                s = at % self.stages
+                yield from self.wait("Y", self.full[s], at // self.stages)
+                if self.ring[s] != (n, ahead):
+                    raise Fault(f"{(n, ahead)} is not in the ring, but {self.ring[s]}")
+                at += 1
+                self.pipe.append(("S", self.s[b]))
+                ahead += 1
+                if ahead == halves:
+                    self.pipe.append(("commit", self.x_empty))
+                stage[b] = s
+
+            yield from self.wait("X", self.x_full, n)
+            for b in range(min(self.bufs, halves)):
+                yield from scores(b)
+            yield from self.wait("accumulators", self.acc_free, n - 1)
+            for g in range(halves):
+                b = g % self.bufs
+                yield from self.wait("P", self.p[b], uses[b])
+                uses[b] += 1
+                self.pipe.append(("PV", self.empty[stage[b]], 0, (n, g)))
+                yield
+                if ahead < halves:
+                    yield from scores(b)
+            self.pipe.append(("commit", self.acc_bar))
+
+    def warp(self, half, w, left):
+        ns, before, slot, joins = 0, [0] * self.bufs, 0, 0  # ns: as the kernel keeps the phases; before: uses of each buffer
+        for n, steps in enumerate(self.items):
+            for i in range(steps):
+                b, other = (2 * i + half) % self.bufs, (2 * i + 1 - half) % self.bufs
+                st = (2 * slot + half) % self.stages
+                slot += 1
+                phase = ns >> b & 1
+                ns ^= 1 << b
+                if self.bufs == 3:
+                    ns ^= 1 << other
+                mine = before[b] + (1 if half == 1 and other == b else 0)
+                assert phase == mine & 1
+                yield from self.wait(f"scores {half}", self.s[b], mine)
+                before[b] += 1
+                before[other] += self.bufs == 3  # with two buffers each half has one
+                yield
+                if self.ring[st] != (n, 2 * i + half) or self.kv and self.far[st] != (n, 2 * i + half):
+                    raise Fault(f"stage {st} holds {self.ring[st]} and {self.far.get(st)}, not {(n, 2 * i + half)}")
+                if not self.kv and steps == 1:
+                    self.sums[half, w] = n
+                    yield
+                    self.d.arrive()
+                    yield from self.wait("sums", self.d, joins)
+                    joins += 1
+                    yield
+                    if self.sums[1 - half, w] != n:
+                        raise Fault(f"half {half} of item {n} reads the other's sums of item {self.sums[1 - half, w]}")
+                self.p[b].arrive()
+                yield
+            yield from self.wait("last product", self.acc_bar, n)
+            if self.acc[0][-1] != (n, 2 * steps - 1):
+                raise Fault(f"the accumulators are read at {self.acc[0][-1]} and not {(n, 2 * steps - 1)}")
+            yield
+            self.acc_free.arrive()
+        left.remove((half, w))
+
+    def run(self):
+        left = {(h, w) for h in (0, 1) for w in range(WARPS)}
+        agents = {x: getattr(self, x)() for x in ("issuer", "tensor", "loader", "copies")}
+        if self.kv:
+            agents["statistics"] = self.statistics()
+        self.go(agents | {x: self.warp(*x, left) for x in left}, left)
+
+
+@pytest.mark.parametrize("bufs", [2, 3])
+@pytest.mark.parametrize("kv", [False, True], ids=["dq", "dkdv"])
+def test_every_wait_of_the_gradients_sees_its_phase(bufs, kv):
+    rng = random.Random(10 + bufs * 2 + kv)
+    for k in range(600):
+        Gradients(bufs, kv, rng.choice([[5, 3, 1, 1], [1, 1, 1, 2, 1], [4, 2, 2, 1], [7, 1, 6], [3, 3, 1, 1, 1]]), rng).run()
