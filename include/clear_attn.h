@@ -501,7 +501,7 @@ CLEAR_API clear_status_t clear_attn_prompt_fwd(const clear_seq_params_t* params,
                                                const clear_seq_view_t* v, const clear_seq_view_t* o, float* lse,
                                                void* stream);
 
-/* Workspace bytes of clear_attn_prompt_bwd (of either type): three fp32 per row and query head, three per row and key/value
+/* Workspace bytes of clear_attn_prompt_bwd (of either type): four fp32 per row and query head, two per row and key/value
  * head and, where few key/value heads leave the GPU idle, fp32 partial sums of dk and dv (at most about 77 MB). They hold for
  * every smaller n_tok with the same heads and d, and do not depend on n_seq. */
 CLEAR_API size_t clear_attn_prompt_bwd_workspace_size(const clear_seq_params_t* params, clear_status_t* status);
@@ -515,8 +515,8 @@ CLEAR_API size_t clear_attn_prompt_bwd_workspace_size(const clear_seq_params_t* 
  * Gradients are written once, in a fixed order of sums: the same call gives the same bits. Rows behind
  * the last sequence are left as they are. As in the forward, sequences do not touch each other, and a
  * NaN within one sequence may reach rows of its own 128-token block before it.
- * Between the products P and dS are rounded to the element type, in fp16 times powers of two taken from the norms of the rows
- * of dO and v: gradients of any size keep fp16's 11 bits there and stay in range (as far as dq, dk and dv themselves do).
+ * Between the products P and dS are rounded to the element type, in fp16 times powers of two taken from the magnitudes of dO
+ * and v: gradients of any size keep fp16's 11 bits there and stay in range (as far as dq, dk and dv themselves do).
  */
 CLEAR_API clear_status_t clear_attn_prompt_bwd(const clear_seq_params_t* params, const int* seq_start,
                                                const clear_seq_view_t* q, const clear_seq_view_t* k,

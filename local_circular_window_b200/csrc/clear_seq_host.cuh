@@ -218,16 +218,18 @@ int bwd_parts(const clear_seq_params_t* p) {
 }
 
 struct PromptBwdWorkspace {
-  size_t norm_g_off, norm_v_off, range_off, part1_off, part2_off, total;
+  size_t mag_g_off, mag_v_off, top_g_off, top_v_off, part1_off, part2_off, total;
 };
 PromptBwdWorkspace prompt_bwd_workspace_layout(const clear_seq_params_t* p) {
   PromptBwdWorkspace w;
   const int parts = bwd_parts(p);
   const size_t sums = parts > 1 ? (size_t)parts * p->kv_heads * p->n_tok * p->d * sizeof(float) : 0;
-  w.norm_g_off = align256((size_t)p->q_heads * p->n_tok * sizeof(float2));  // (-lse, -D) before
-  w.norm_v_off = w.norm_g_off + align256((size_t)p->q_heads * p->n_tok * sizeof(float));
-  w.range_off = w.norm_v_off + align256((size_t)p->kv_heads * p->n_tok * sizeof(float));
-  w.part1_off = w.range_off + align256((size_t)p->kv_heads * p->n_tok * sizeof(float2));
+  const size_t g = align256((size_t)p->q_heads * p->n_tok * sizeof(float)), v = align256((size_t)p->kv_heads * p->n_tok * sizeof(float));
+  w.mag_g_off = align256((size_t)p->q_heads * p->n_tok * sizeof(float2));  // (-lse, -D) before
+  w.mag_v_off = w.mag_g_off + g;
+  w.top_g_off = w.mag_v_off + v;
+  w.top_v_off = w.top_g_off + g;
+  w.part1_off = w.top_v_off + v;
   w.part2_off = w.part1_off + align256(sums);
   w.total = w.part2_off + align256(sums);
   return w;
@@ -245,7 +247,7 @@ size_t prompt_bwd_workspace_most(const clear_seq_params_t* p) {
   return most;
 }
 
-constexpr int kRangeBlocks = 1024;  // along the sequences
+constexpr int kTopsBlocks = 128;  // along the sequences
 
 template <typename E, int D>
 clear_status_t launch_prompt_bwd(const clear_seq_params_t* sp, const SeqView& q, const SeqView& k, const SeqView& v, const SeqView& g,
@@ -271,8 +273,8 @@ clear_status_t launch_prompt_bwd(const clear_seq_params_t* sp, const SeqView& q,
   p.out2 = dq;  // first: it settles the first rows' statistics for the other
   const unsigned q_blocks = prompt_blocks(sp, 128, sp->q_heads, num_sms);
   if (kF16) {
-    const dim3 range(sp->n_seq < kRangeBlocks ? sp->n_seq : kRangeBlocks, sp->kv_heads);
-    if (!launch_dependent(clear_seq_bwd_range_kernel, range, kRangeThreads, 0, stream, p) ||
+    const dim3 tops(sp->n_seq < kTopsBlocks ? sp->n_seq : kTopsBlocks, sp->q_heads);
+    if (!launch_dependent(clear_seq_bwd_tops_kernel, tops, kTopsThreads, 0, stream, p) ||
         !launch_dependent(clear_seq_prompt_bwd_kernel<E, D, false>, q_blocks, kPrThreads, LQ::kAlloc, stream, mq, mg, sk, sv, p))
       return CLEAR_ERR_CUDA;
   } else {
@@ -448,12 +450,14 @@ clear_status_t clear_attn_prompt_bwd(const clear_seq_params_t* params, const int
   SeqBwdParams p{};
   p.stats = sp.stats;
   const PromptBwdWorkspace wl = prompt_bwd_workspace_layout(params);
-  p.norm_g = sp.norm_g = reinterpret_cast<float*>(static_cast<char*>(workspace) + wl.norm_g_off);
-  p.norm_v = sp.norm_v = reinterpret_cast<float*>(static_cast<char*>(workspace) + wl.norm_v_off);
-  p.range = reinterpret_cast<float2*>(static_cast<char*>(workspace) + wl.range_off);
+  const auto at = [&](size_t off) { return reinterpret_cast<float*>(static_cast<char*>(workspace) + off); };
+  p.mag_g = sp.mag_g = at(wl.mag_g_off);
+  p.mag_v = sp.mag_v = at(wl.mag_v_off);
+  p.top_g = at(wl.top_g_off);
+  p.top_v = at(wl.top_v_off);
   p.parts = bwd_parts(params);
-  p.part1 = reinterpret_cast<float*>(static_cast<char*>(workspace) + wl.part1_off);
-  p.part2 = reinterpret_cast<float*>(static_cast<char*>(workspace) + wl.part2_off);
+  p.part1 = at(wl.part1_off);
+  p.part2 = at(wl.part2_off);
   p.seq_start = sp.seq_start = seq_start;
   p.n_seq = sp.n_seq = params->n_seq;
   p.n_tok = sp.n_tok = params->n_tok;

@@ -4,8 +4,8 @@
 //   dV = P^T dO,  dK = dS^T Q / sqrt(d), both summed over the query heads of the group;  dQ = dS K / sqrt(d).
 //
 // Three launches (fp16: four), deterministic, without atomics:
-//   stats   (-lse, -D) of every row, one pass over o and dO (bound by memory); fp16: norms of dO's and v's rows
-//   range   fp16: the largest norms of each sequence and kv head
+//   stats   (-lse, -D) of every row, one pass over o and dO (bound by memory); fp16: magnitudes of dO's and v's rows
+//   tops    fp16: the largest magnitudes of each sequence and head
 //   q       one item per 128-row query tile and query head: Q and dO stay, K and V stream past
 //   kv      one item per 128-key tile and kv head: K and V stay, the group's Q and dO stream past
 // S and dP are computed in both, seven products in place of five: the price of writing every gradient
@@ -36,11 +36,11 @@
 // P and dS are rounded to the element type; sums, statistics and accumulators are fp32. In bf16 that is half a step of each, 2^-8
 // at most. fp16's steps are absolute below 2^-14, where P (about 1 / keys) and dS = P (dP - D) of small gradients lie, and its
 // range ends at 2^16. So fp16 holds P times 2^14 (P <= 1), and dS times a power of two from the bound
-//   |dS_ij| <= |dP_ij| + |D_i| <= 2 |dO_i| |v|max   (norms of rows; |v|max over the sequence and kv head)
-// that brings the bound to 2^13 ... 2^14: one per row in the q kernel, one per sequence and kv head (with the largest |dO_i| of the
-// group's heads) in kv. Both are taken out again from the fp32 accumulators. dS of any fp16 input is then in range, and half a
-// step is 2^-11 of each down to 2^-27 of its bound, an absolute 2^-38 of the bound below. The norms ride along in the statistics' pass; a
-// small kernel finds their maxima.
+//   |dS_ij| <= |dP_ij| + |D_i| <= 2 d max|dO_i| max|v|   (the row's largest magnitude; that of v in the sequence and kv head)
+// that brings the bound to 2^13 ... 2^14: one per row in the q kernel, one per sequence and part of a group (with the largest |dO_i| of
+// its heads) in kv. Both are taken out again from the fp32 accumulators. dS of any fp16 input is then in range, and half a
+// step is 2^-11 of each down to 2^-27 of its bound, an absolute 2^-38 of the bound below. The rows' magnitudes ride along in the
+// statistics' pass; a small kernel finds the sequences'.
 //
 // D from the given o carries o's rounding, which dS = P (dP - D) shares along the whole row: against the
 // rounding of dS itself that is about one part in sqrt(keys), so it shows only in a sequence's first
@@ -65,19 +65,19 @@ struct SeqBwdParams {
   int parts;
   float *part1, *part2;
   float2* stats;         // [q_heads, n_tok]: (-lse, -D)
-  // fp16: norms of the rows of dO [q_heads, n_tok] and of v [kv_heads, n_tok]; the largest of each in a sequence (of dO: of the
-  // group's heads) [kv_heads, n_tok], at the sequence's first token.
-  float *norm_g, *norm_v;
-  float2* range;
+  // fp16: largest magnitudes: of each row of dO [q_heads, n_tok] and of v [kv_heads, n_tok], and of a whole sequence in each head, the
+  // same, at the sequence's first token.
+  float *mag_g, *mag_v, *top_g, *top_v;
   const int* seq_start;
   int n_seq, n_tok, q_heads, kv_heads, group;
   float scale, scale_log2;
 };
 
-// The power of two that brings 2 a b, the bound of |dS| of rows with norms a and b, to [2^13, 2^14). Zero, infinite and NaN bounds
-// stay: such rows hold nothing that could be kept.
+// The power of two that brings 2 d a b, the bound of |dS| of rows with magnitudes a and b, to [2^13, 2^14). Zero, infinite and NaN
+// bounds stay: such rows hold nothing that could be kept.
+template <int D>
 __device__ __forceinline__ int lift_of(float a, float b) {
-  const float bound = 2.f * a * b;
+  const float bound = (2.f * D) * a * b;
   return bound > 0.f && bound < INFINITY ? 13 - ilogbf(bound) : 0;
 }
 constexpr float kBwdLift = 14.f;  // fp16: P is held times 2^14
@@ -87,12 +87,19 @@ struct SeqStatsParams {
   SeqView o, g, v;
   const float* lse;
   float2* stats;
-  float *norm_g, *norm_v;
+  float *mag_g, *mag_v;
   const int* seq_start;
   int n_seq, n_tok, q_heads, group;
 };
 
 constexpr int kStatsThreads = 256;
+
+// The larger magnitude of each half of two pairs of fp16 (NaN gives way).
+__device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
+  return r;
+}
 
 // D / 8 lanes take one row of o and dO, in fp16 those of a group's first head also one of v.
 template <typename E, int D>
@@ -101,7 +108,7 @@ __global__ void __launch_bounds__(kStatsThreads) clear_seq_bwd_stats_kernel(cons
   constexpr int kLanes = D / 8;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x % kLanes;
-  constexpr bool kNorms = !std::is_same<E, Bf16>::value;
+  constexpr bool kMags = !std::is_same<E, Bf16>::value;
   const long long row = ((long long)blockIdx.x * kStatsThreads + threadIdx.x) / kLanes;  // token-major: heads are next to each other
   const long long t = row / p.q_heads;
   const int h = (int)(row - t * p.q_heads);
@@ -119,77 +126,98 @@ __global__ void __launch_bounds__(kStatsThreads) clear_seq_bwd_stats_kernel(cons
     end = __reduce_max_sync(0xffffffffu, top);
   }
   const bool in = t < end;
-  const int hk = kNorms ? h / p.group : 0;
-  const bool first = kNorms && h == hk * p.group;
-  float sum = 0.f, square_g = 0.f, square_v = 0.f;
+  const int hk = kMags ? h / p.group : 0;
+  const bool first = kMags && h == hk * p.group;
+  float sum = 0.f;
+  uint32_t mag = 0;  // largest magnitudes of dO (low) and v
   if (in) {
     const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.o.ptr) + h * p.o.sh + t * p.o.st) + lane);
     const uint4 b = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.g.ptr) + h * p.g.sh + t * p.g.st) + lane);
     uint4 c = make_uint4(0, 0, 0, 0);
     if (first) c = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.v.ptr) + hk * p.v.sh + t * p.v.st) + lane);
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w}, z[4] = {c.x, c.y, c.z, c.w};
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
     #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      sum = fmaf(E::hi(x[e]), E::hi(y[e]), fmaf(E::lo(x[e]), E::lo(y[e]), sum));
-      if (kNorms) {
-        square_g = fmaf(E::hi(y[e]), E::hi(y[e]), fmaf(E::lo(y[e]), E::lo(y[e]), square_g));
-        square_v = fmaf(E::hi(z[e]), E::hi(z[e]), fmaf(E::lo(z[e]), E::lo(z[e]), square_v));
-      }
+    for (int e = 0; e < 4; ++e) sum = fmaf(E::hi(x[e]), E::hi(y[e]), fmaf(E::lo(x[e]), E::lo(y[e]), sum));
+    if (kMags) {
+      const uint32_t g = max_abs(max_abs(b.x, b.y), max_abs(b.z, b.w)), v = max_abs(max_abs(c.x, c.y), max_abs(c.z, c.w));
+      mag = max_abs(__byte_perm(g, v, 0x5410), __byte_perm(g, v, 0x7632));
     }
   }
   #pragma unroll
   for (int d = kLanes / 2; d > 0; d >>= 1) {
     sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (kNorms) {
-      square_g += __shfl_xor_sync(0xffffffffu, square_g, d);
-      square_v += __shfl_xor_sync(0xffffffffu, square_v, d);
-    }
+    if (kMags) mag = max_abs(mag, __shfl_xor_sync(0xffffffffu, mag, d));
   }
   if (in && lane == 0) {
     const float l = __ldg(p.lse + (long long)h * p.n_tok + t);
     // A row without a finite score (lse -inf) has P = 0: 2^(-inf) instead of 2^(-inf + inf).
     p.stats[(long long)h * p.n_tok + t] = make_float2(l == -INFINITY ? -INFINITY : -l, -sum);
-    if (kNorms) p.norm_g[(long long)h * p.n_tok + t] = sqrtf(square_g);
-    if (first) p.norm_v[(long long)hk * p.n_tok + t] = sqrtf(square_v);
+    if (kMags) p.mag_g[(long long)h * p.n_tok + t] = Fp16::lo(mag);
+    if (first) p.mag_v[(long long)hk * p.n_tok + t] = Fp16::hi(mag);
   }
 }
 
-// The largest norms of a sequence's rows: a block takes one sequence and kv head at a time. Whether a NaN takes part does not matter.
-// It and the q kernel behind it are programmatic dependents: their launches hide behind the kernel before.
-constexpr int kRangeThreads = 512;
-__global__ void __launch_bounds__(kRangeThreads) clear_seq_bwd_range_kernel(const __grid_constant__ SeqBwdParams p) {
-  __shared__ float2 best[kRangeThreads / 32];
-  const int hk = blockIdx.y, tid = threadIdx.x;
+// The largest magnitudes of each sequence's rows in head blockIdx.y of dO, and of v with the first head of its group: a block takes
+// every gridDim.x-th sequence, up to 128 rows by one warp, more by all. Whether a NaN takes part does not matter. It and the q
+// kernel behind it are programmatic dependents: their launches hide behind the kernel before.
+constexpr int kTopsThreads = 512, kTopsWarps = kTopsThreads / 32;
+constexpr int kTopsAlone = 128;
+__global__ void __launch_bounds__(kTopsThreads) clear_seq_bwd_tops_kernel(const __grid_constant__ SeqBwdParams p) {
+  __shared__ float2 best[kTopsWarps];
+  const int h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hk = h / p.group;
+  const bool with_v = h == hk * p.group;
+  const float* const mag_g = p.mag_g + (long long)h * p.n_tok;
+  const float* const mag_v = p.mag_v + (long long)hk * p.n_tok;
+  float* const top_g = p.top_g + (long long)h * p.n_tok;
+  float* const top_v = p.top_v + (long long)hk * p.n_tok;
   asm volatile("griddepcontrol.wait;\ngriddepcontrol.launch_dependents;" ::: "memory");
-  for (int s = blockIdx.x; s < p.n_seq; s += gridDim.x) {
-    int first, len;
-    seq_range(p.seq_start, p.n_tok, s, &first, &len);
-    if (len == 0) continue;
+  // Over the rows from, from + step, ...: the largest in the warp.
+  const auto largest = [&](int first, int len, int from, int step) {
     float g = 0.f, v = 0.f;
-    const float* src = p.norm_v + (long long)hk * p.n_tok + first;
     #pragma unroll 4
-    for (int i = tid; i < len; i += kRangeThreads) v = fmaxf(v, src[i]);
-    for (int h = hk * p.group; h < (hk + 1) * p.group; ++h) {
-      src = p.norm_g + (long long)h * p.n_tok + first;
-      #pragma unroll 4
-      for (int i = tid; i < len; i += kRangeThreads) g = fmaxf(g, src[i]);
+    for (int i = from; i < len; i += step) {
+      g = fmaxf(g, mag_g[first + i]);
+      if (with_v) v = fmaxf(v, mag_v[first + i]);
     }
     #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
       g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, d));
       v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
     }
-    if ((tid & 31) == 0) best[tid >> 5] = make_float2(g, v);
-    __syncthreads();
-    if (tid == 0) {
-      #pragma unroll
-      for (int i = 1; i < kRangeThreads / 32; ++i) {
-        g = fmaxf(g, best[i].x);
-        v = fmaxf(v, best[i].y);
+    return make_float2(g, v);
+  };
+  const auto store = [&](int first, float2 x) {
+    top_g[first] = x.x;
+    if (with_v) top_v[first] = x.y;
+  };
+  for (long long s0 = blockIdx.x; s0 < p.n_seq; s0 += (long long)kTopsWarps * gridDim.x) {
+    int first, len;
+    const long long mine = s0 + (long long)warp * gridDim.x;
+    if (mine < p.n_seq) {
+      seq_range(p.seq_start, p.n_tok, (int)mine, &first, &len);
+      if (len > 0 && len <= kTopsAlone) {
+        const float2 x = largest(first, len, lane, 32);
+        if (lane == 0) store(first, x);
       }
-      p.range[(long long)hk * p.n_tok + first] = make_float2(g, v);
     }
-    __syncthreads();
+    for (long long s = s0; s < p.n_seq && s < s0 + (long long)kTopsWarps * gridDim.x; s += gridDim.x) {
+      seq_range(p.seq_start, p.n_tok, (int)s, &first, &len);
+      if (len <= kTopsAlone) continue;
+      const float2 x = largest(first, len, tid, kTopsThreads);
+      if (lane == 0) best[warp] = x;
+      __syncthreads();
+      if (warp == 0) {
+        float2 y = best[lane % kTopsWarps];
+        #pragma unroll
+        for (int d = kTopsWarps / 2; d > 0; d >>= 1) {
+          y.x = fmaxf(y.x, __shfl_xor_sync(0xffffffffu, y.x, d));
+          y.y = fmaxf(y.y, __shfl_xor_sync(0xffffffffu, y.y, d));
+        }
+        if (lane == 0) store(first, y);
+      }
+      __syncthreads();
+    }
   }
 }
 
@@ -228,9 +256,8 @@ struct PromptBwdLayout {
   static constexpr int kNumBars = bD + 1;
   static constexpr int kItems = (kBars + kNumBars * 8 + 15) & ~15;
   static constexpr int kMisc = kItems + kPrItems * 16;
-  static constexpr int kTops = kMisc + 16;                 // float[kPrItems]
-  static constexpr int kFar = kTops + kPrItems * 4;        // int[kStages]: fp16: whether a half has rows that are far
-  static constexpr int kAlloc = kFar + kStages * 4 + 1024;
+  static constexpr int kInfo = kMisc + 16;                 // int[kStages]; fp16: see below
+  static constexpr int kAlloc = kInfo + kStages * 4 + 1024;
   static_assert(kAlloc <= 232448, "shared memory");
 };
 
@@ -292,8 +319,8 @@ __device__ __noinline__ void add_far(uint32_t s_tm, const float2* stats, int lef
   tmem_wait_st();
 }
 
-// An item as the ring carries it: {the sequence's first token, its length (0: end of the list), X tile, head}; fp16: and beside it
-// the largest norm of v's rows (q) or the power of two in dS (kv).
+// An item as the ring carries it: {the sequence's first token, its length (0: end of the list), X tile, head}.
+// fp16, kv: with a half's statistics comes a word, 2 * (the power of two in dS) + (whether a row is far).
 template <typename E, int D, bool kKv>
 __global__ void __launch_bounds__(kPrThreads, 1)
 clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_x2,
@@ -306,8 +333,7 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
   uint8_t* smem = align1024(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
   int4* items = reinterpret_cast<int4*>(smem + L::kItems);
-  float* tops = reinterpret_cast<float*>(smem + L::kTops);
-  int* far = reinterpret_cast<int*>(smem + L::kFar);
+  int* info = reinterpret_cast<int*>(smem + L::kInfo);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -355,12 +381,10 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
   const uint32_t tmem = *tmem_slot;
 
   uint32_t n_item = 0;
-  float item_top = 0.f;
   const auto next_item = [&](int4* it, int site) -> bool {
     const uint32_t s = n_item % kPrItems;
     if (!warp_wait(&bars[L::bItemFull + s], (n_item / kPrItems) & 1, abort_flag, kDevTimeoutOther, site, (int)n_item)) return false;
     *it = items[s];
-    if (kF16) item_top = tops[s];
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[L::bItemEmpty + s]);
     ++n_item;
@@ -539,17 +563,12 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
       const long long x = deal(r, blockIdx.x, gridDim.x);
       int4 it = make_int4(0, 0, 0, 0);
       const bool more = x < total;
-      float top = 0.f;
       if (more) {
         int lv;  // steps: level + 1 query tiles (kv: those from the key tile on) or key tiles (q)
         const int s = list.find(x / heads, &lv);
         int first, len;
         seq_range(p.seq_start, p.n_tok, s, &first, &len);
         it = make_int4(first, len, kKv ? ((len + 127) >> 7) - 1 - lv : lv, (int)(x % heads));
-        if (kF16) {
-          const float2 norms = p.range[(long long)(kKv ? it.w / p.parts : it.w / p.group) * p.n_tok + first];
-          top = kKv ? (float)lift_of(norms.x, norms.y) : norms.y;
-        }
       } else if ((long long)r * gridDim.x < total) {
         continue;
       }
@@ -557,7 +576,6 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
       if (!warp_wait(&bars[L::bItemEmpty + s], ((n / kPrItems) & 1) ^ 1, abort_flag, kDevTimeoutOther, 3, (int)n)) break;
       if (lane == 0) {
         items[s] = it;
-        if (kF16) tops[s] = top;
         mbar_arrive(&bars[L::bItemFull + s]);
       }
       __syncwarp();
@@ -573,6 +591,13 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
       bool ok = true;
       while (ok && next_item(&it, 52)) {
         const int steps = steps_of(it), per = n_tiles(it) - it.z, head0 = h_first(it);
+        // The item's power of two: its loads are under way with those of the first half's statistics.
+        int lift = 0;
+        float top_g = 0.f, top_v = 0.f;
+        if (kF16) {
+          for (int h = lane; h < h_count(it); h += 32) top_g = fmaxf(top_g, p.top_g[(long long)(head0 + h) * p.n_tok + it.x]);
+          top_v = p.top_v[(long long)(it.w / p.parts) * p.n_tok + it.x];
+        }
         for (int i = 0; i < 2 * steps; ++i, ++slot) {
           const int t0 = (it.z + (i >> 1) % per) * 128 + (i & 1) * 64;
           const float2* src = p.stats + (long long)(head0 + (i >> 1) / per) * p.n_tok + it.x + t0;
@@ -582,6 +607,11 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
           const uint32_t s = slot % L::kStages;
           ok = warp_wait(&bars[L::bYEmpty + s], ((slot / L::kStages) & 1) ^ 1, abort_flag, kDevTimeoutOther, 4, (int)slot);
           if (!ok) break;
+          if (kF16 && i == 0) {
+            #pragma unroll
+            for (int d = 16; d > 0; d >>= 1) top_g = fmaxf(top_g, __shfl_xor_sync(0xffffffffu, top_g, d));
+            lift = lift_of<D>(top_g, top_v);
+          }
           bool any = false;
           #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -598,7 +628,7 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
           }
           if (kF16) {
             any = __any_sync(0xffffffffu, any);
-            if (lane == 0) far[s] = any;
+            if (lane == 0) info[s] = 2 * lift + (int)any;
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -624,14 +654,14 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
       const bool valid = it.z * 128 + row < it.y;
       const long long tok = (long long)it.x + it.z * 128 + row;
       float2 mine = make_float2(0.f, 0.f);
-      int lift = 0;  // fp16: the power of two in dS: of this row, or (kv) of the sequence and kv head
+      int lift = 0;  // fp16: the power of two in dS
       if (!kKv && valid) {
         mine = p.stats[(long long)it.w * p.n_tok + tok];
+        const float a = kF16 ? p.mag_g[(long long)it.w * p.n_tok + tok] : 0.f;
+        const float b = kF16 ? p.top_v[(long long)(it.w / p.group) * p.n_tok + it.x] : 0.f;
         mine.x *= 1.4426950408889634f;
+        if (kF16) lift = lift_of<D>(a, b);
       }
-      if (kF16) lift = kKv ? (int)item_top : lift_of(valid ? p.norm_g[(long long)it.w * p.n_tok + tok] : 0.f, item_top);
-      const float more = kF16 && kKv ? pow2(lift - (int)kBwdLift) : 1.f;  // P has its own
-      const uint64_t more2 = f32x2_pack(more, more);
       for (int i = 0; i < steps; ++i, ++slot) {
         const uint32_t buf = (2 * i + half) % L::kBufs;
         const int yt = kKv ? it.z + i % per : i;
@@ -663,9 +693,16 @@ clear_seq_prompt_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __g
           }
           fence_proxy_async_smem();
         }
-        if (kF16 && kKv && far[st]) {
-          const int t0 = yt * 128 + half * 64;
-          add_far(s_tm, p.stats + (long long)(h_first(it) + i / per) * p.n_tok + it.x + t0, it.y - t0, root);
+        uint64_t more2 = 0;  // fp16, kv: from P's power of two to dS's
+        if (kF16 && kKv) {
+          const int word = info[st];
+          lift = word >> 1;
+          const float more = pow2(lift - (int)kBwdLift);
+          more2 = f32x2_pack(more, more);
+          if (word & 1) {
+            const int t0 = yt * 128 + half * 64;
+            add_far(s_tm, p.stats + (long long)(h_first(it) + i / per) * p.n_tok + it.x + t0, it.y - t0, root);
+          }
         }
         const bool all = lo <= 0 && hi >= 64;
         const bool warp_all = __all_sync(0xffffffffu, all);
