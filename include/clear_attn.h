@@ -408,7 +408,8 @@ CLEAR_API clear_status_t clear_attn_selftest_expiry(int limit_ms, void* stream);
  * when the kernels run: a captured graph may be replayed with other contents. The kernels check them. A
  * sequence whose offsets decrease or leave [0, n_tok] is skipped, one longer than max_pages pages is cut,
  * a page number outside [0, n_pages) reads as zeros and is not written, and clear_attn_check() reports
- * CLEAR_ERR_DEVICE_INDEX. Tokens behind the last sequence do not count and are not written.
+ * CLEAR_ERR_DEVICE_INDEX. Tokens behind the last sequence do not count and are not written. Where offsets that do not ascend give
+ * a token to two valid sequences, that token's results, and what its sequences draw from them, are undefined.
  *
  * Statuses: CLEAR_ERR_INVALID_ARG for null or misaligned (16 bytes) pointers, sizes out of range
  * (n_seq in [1, 2^20], n_tok in [1, 2^30]), q_heads not a multiple of kv_heads;
@@ -462,6 +463,7 @@ typedef struct {
  *   k, v    new keys and values; rotated keys and values go to the cache (E4M3: rounded to nearest
  *           from the fp32 rotated value over the scale, saturated at 448).
  *   k_out   NULL, or receives the rotated keys (packed), and may be k itself.
+ * E4M3 scales have to be normal numbers between 2^-126 and 2^126 (their reciprocal is taken).
  * Only the new tokens' rows of the cache are written. Two tokens that the page table sends to the
  * same row (a page listed twice where both write) leave that row undefined.
  */
@@ -512,6 +514,7 @@ CLEAR_API size_t clear_attn_prompt_bwd_workspace_size(const clear_seq_params_t* 
  * dK and dV summed over the query heads that share them.
  *   q, o, dO, dq [q_heads, n_tok, d]; k, v, dk, dv [kv_heads, n_tok, d]; lse fp32 [q_heads, n_tok]
  *   workspace: clear_attn_prompt_bwd_workspace_size bytes, 256-byte aligned; contents undefined on return
+ * P = e^(S - lse) is as exact as the fp32 lse: with scores of a million, lse has steps of 1/16.
  * Gradients are written once, in a fixed order of sums: the same call gives the same bits. Rows behind
  * the last sequence are left as they are. As in the forward, sequences do not touch each other, and a
  * NaN within one sequence may reach rows of its own 128-token block before it.

@@ -15,8 +15,7 @@
 // Work split. The unit is a (sequence, kv head, 16 heads of its group); its keys are cut into
 // tiles of 64. All units' tiles form one line, and each of the grid's blocks takes an equal piece of it, so
 // ragged batches and single long sequences load every SM alike. A unit's start counts as some tiles more: finishing a
-// piece costs about a microsecond, so a block with many short units has fewer tiles (48 sequences of 128 to
-// 8192 tokens in bf16: 83 us without, 71 us with; 96 of 94 to 6000 in E4M3: 92 and 70 us, with two blocks per SM). A piece that is not a whole unit
+// piece costs about a microsecond, so a block with many short units has fewer tiles (kUnitCost). A piece that is not a whole unit
 // leaves (m, l, O) in the workspace, and a second small kernel joins the pieces of a unit in
 // their order along the keys: no atomics, the same bits on every run. It is launched as a
 // programmatic dependent, so its launch hides behind the first kernel.
@@ -119,7 +118,10 @@ struct DecLayout {
   static constexpr int kBoxes = kRowBytes / kBox;
   static constexpr int kSide = kDecSlice * kRowBytes;                // the slice's keys; its values follow
   static constexpr int kSliceBytes = 2 * kSide;
-  static constexpr int kUnitCost = kRowBytes >= 256 ? 2 : 4;         // tiles' time that finishing a unit takes
+  // Tiles' time that finishing a unit takes: about a microsecond, and a tile of 256-byte rows takes half of one. Measured with 0, 1,
+  // 2, 4 and 8 on 256 sequences of 23 to 1500 tokens: 256-byte rows (bf16, d = 128) 99, 89, 88, 89 and 94 us; 128 bytes (bf16, d = 64) 72,
+  // 65, 58, 56 and 62, (E4M3, d = 128) 90, 73, 67, 58 and 64; 64 bytes 72, 58, 53, 47 and 51.
+  static constexpr int kUnitCost = kRowBytes >= 256 ? 2 : 4;
   static constexpr int kStages = kRing / kSliceBytes < kDecMaxStages ? kRing / kSliceBytes : kDecMaxStages;
   static constexpr int kRows = 8 * kN;
   static constexpr int kJoin = kDecWarps * kStages * kSliceBytes;    // O of the four warps, then their (m, l)

@@ -95,7 +95,10 @@ clear_status_t check_seq_cache(const clear_seq_params_t* p, const clear_seq_cach
 }
 
 // ---------------------------------------------------------------------------------------- append
-constexpr int kAppendMany = 1024;  // tokens from which blocks are small
+// Tokens from which blocks are small (128 threads): enough blocks then to fill the SMs with such. Measured small and large, 24 and 8
+// heads of 128, bf16: 256 tokens 4.4 and 3.9 us, 512 tokens 5.0 and 4.6, 1024 tokens 6.0 and 6.8, 8192 tokens 33 and 41; 32 and 8
+// into E4M3: 256 tokens 4.9 and 4.2, 512 tokens 5.6 and 6.4, 1024 tokens 6.5 and 8.9. Few heads have small blocks anyway.
+constexpr int kAppendMany = 1024;
 
 template <typename E, bool kF8, int D, bool kHalves>
 clear_status_t launch_append(const SeqAppendParams& a, cudaStream_t stream) {
@@ -194,9 +197,12 @@ clear_status_t launch_prompt_fwd(const clear_seq_params_t* sp, const SeqView& q,
   if (!make_seq_map(&mq, q, sp->q_heads, sp->n_tok, D, sp->dtype) || !make_seq_map(&mk, k, sp->kv_heads, sp->n_tok, D, sp->dtype) ||
       !make_seq_map(&mv, v, sp->kv_heads, sp->n_tok, D, sp->dtype))
     return CLEAR_ERR_CUDA;
-  // Whole items share each key tile between 256 rows; split ones are twice as many and half as long. Measured at d = 128, whole
-  // and split: one sequence of 6000 tokens, 2 heads (48 items) 85 and 49 us; 8 heads (192) 88 and 77 us; six of 683 on
-  // average, 16 heads (256) 58 and 47 us; two of 2048, 24 heads (384) 66 and 75 us. Short sequences have short items
+  // Whole items share each key tile between 256 rows; split ones are twice as many and half as long, which pays where a block's one
+  // or two long items bound the whole. Measured whole and split at d = 128 (at d = 64): one sequence of 6000 tokens, 2 heads (48 items)
+  // 86 and 49 us (81 and 44); 8 heads (192) 89 and 77 (84 and 68); one of 12000, 4 heads (188) 173 and 134 (162 and 120); six
+  // of 683 on average and unlike, 16 heads (256) 58 and 47; two of 2048, 24 heads (384) 65 and 74 (57 and 64); one of 4096, 32
+  // heads (512) 128 and 141 (116 and 120). Between 190 and 300 items it depends on how unlike the lengths are, which the host does not
+  // see: like ones lose, six of 683 each 29 and 36 us, one of 4096 with 16 heads 67 and 74. Short sequences have short items
   // already: eight of 300, 8 heads (80) 13 and 16 us.
   const bool split = ((long long)sp->n_tok + 255) / 256 * sp->q_heads < kPrSplitItems && sp->n_tok >= 512ll * sp->n_seq;
   static std::atomic<unsigned long long> done[2];
