@@ -268,7 +268,7 @@ def clear_attn_prompt_fwd(q, k, v, seq_start, o=None, lse=None, stream=None):
 
 
 def prompt_bwd_workspace_size(n_tok: int, q_heads: int, kv_heads: int, d: int) -> int:
-    """Bytes of clear_attn_prompt_bwd's workspace."""
+    """Bytes of clear_attn_prompt_bwd's workspace, of either type, for n_tok tokens or fewer."""
     return _size(_lib.clear_attn_prompt_bwd_workspace_size, _pack_params(1, n_tok, q_heads, kv_heads, d, 0))
 
 
